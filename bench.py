@@ -337,7 +337,7 @@ def measure(moe, synth, torch, np, name, seed, steps, warmup, cold_reps, stream)
 
     # per-kernel durations (3 launches each) to name the dominant kernel
     # the kernels one step launches (the router is timed on its own)
-    step_kernels = [k for k in moe.KERNELS if not k.startswith("route")]
+    step_kernels = moe.KERNELS[:moe.KERNELS.index("route")]  # those of the bf16 step
     kernels = step_kernels if backward else step_kernels[:step_kernels.index("combine") + 1]
     kernel_us = {}
     for k in kernels:

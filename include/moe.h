@@ -185,10 +185,107 @@ moe_status moe_expert_backward(const moe_metadata *meta, const int32_t *topk_idx
                                void *dw_down, float *d_topk_weights, void *workspace,
                                size_t workspace_bytes, void *stream);
 
+/* ---- 8-bit operands with a scale for each block of 128 --------------------------
+ * The expert layer on e4m3 operands (the OCP 8-bit format with 4 exponent and 3
+ * mantissa bits, largest value 448, no infinities), with what a program needs ahead of
+ * it: an RMS norm that hands its output on in 8 bits, and the quantisation of rows and
+ * of weights.
+ *
+ * Blocks and scales. Rows of activations have one scale per MOE_QBLOCK consecutive
+ * values (the last block of a row may be shorter); weights one per block of
+ * MOE_QBLOCK x MOE_QBLOCK. A value stands for e4m3 * scale. Scale tensors are dense:
+ * [rows, ceil(L/128)] and [E, ceil(out/128), ceil(in/128)].
+ *  MOE_SCALE_FP32: fp32 scales. The products take any positive finite ones (those of a
+ *                  checkpoint, or of a dispatch); scale products are formed in fp32, so
+ *                  the product of a row's and a weight's scale has to be a normal number.
+ *  MOE_SCALE_E8M0: one byte b for the power of two 2^(b-127), 0 <= b <= 254 (255 is NaN).
+ * The scales this library writes are powers of two in either form: the least s with
+ * max|v| <= 448 s over the block's finite values, at least 2^-126. Quotients v/s are
+ * then exact, and each value is rounded once: to nearest, ties to even. A value that is
+ * not finite becomes NaN (and nothing else in its block changes).
+ * e4m3 rows and weights need lengths that are multiples of 16 in the products. */
+typedef enum { MOE_SCALE_FP32 = 0, MOE_SCALE_E8M0 = 1 } moe_scale_type;
+enum { MOE_QBLOCK = 128 };
+
+/* Rows in 8 bits: x [N,H] (dt) -> q [N,H] e4m3, scale [N, ceil(H/128)]. H a positive
+ * multiple of 8 up to 2^20. */
+moe_status moe_quantize_rows(const void *x, int32_t N, int32_t H, moe_dtype dt, void *q,
+                             void *scale, moe_scale_type scale_type, void *stream);
+
+/* Weights in 8 bits, transposed for the products: w [E,K,C] (dt, as moe_expert_forward
+ * takes W_up and W_down: K in, C out) -> q [E,C,K] e4m3, scale [E, ceil(C/128),
+ * ceil(K/128)]. K and C positive multiples of 16 up to 2^20 (C: 2^21). */
+moe_status moe_quantize_weights(const void *w, int32_t E, int32_t K, int32_t C, moe_dtype dt,
+                                void *q, void *scale, moe_scale_type scale_type,
+                                void *stream);
+
+/* RMS norm with the residual's addition:
+ *   r = x + residual, rounded to dt (r = x when residual is NULL);
+ *   rstd = 1 / sqrt(mean(r^2) + eps);  y = r * rstd * weight.
+ * x, residual, residual_out [N,H], weight [H] in dt. residual_out receives r (required
+ * with a residual, NULL without; it may be x or residual itself). y [N,H] (dt), or NULL;
+ * q [N,H] e4m3 with scale [N, ceil(H/128)], or NULL; one of the two at least. Both are
+ * rounded from the unrounded fp32 y. rstd [N] fp32, or NULL (the backward takes it).
+ * H a positive multiple of 8 up to 2^20; eps >= 0. Sums are fp32 in a fixed order. */
+moe_status moe_rmsnorm_forward(const void *x, const void *residual, const void *weight,
+                               float eps, int32_t N, int32_t H, moe_dtype dt,
+                               void *residual_out, void *y, void *q, void *scale,
+                               moe_scale_type scale_type, float *rstd, void *stream);
+
+/* Backward of moe_rmsnorm_forward for dy [N,H], the gradient of y (and, with the rounding
+ * to 8 bits taken as the identity, of the values q stands for), and dresidual [N,H], that
+ * of residual_out from its other readers (NULL: none). r is residual_out (x without a
+ * residual), rstd as written by the forward:
+ *   g = dy * weight;  dx = rstd * (g - r * rstd^2 * mean(g * r)) + dresidual;
+ *   dweight = sum over the rows of dy * r * rstd.
+ * dx [N,H] is the gradient of x and of residual alike (it may be dresidual or dy itself);
+ * dweight [H]; both in dt, fully overwritten (dweight zeros when N = 0). Sums are fp32 in
+ * a fixed order. workspace >= moe_rmsnorm_backward_workspace(N, H). */
+size_t moe_rmsnorm_backward_workspace(int32_t N, int32_t H);
+moe_status moe_rmsnorm_backward(const void *dy, const void *r, const void *weight,
+                                const float *rstd, const void *dresidual, int32_t N, int32_t H,
+                                moe_dtype dt, void *dx, void *dweight, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* Matrix products grouped by expert on e4m3 operands: for the sorted positions s of
+ * expert e (expert_frequency_offset[e] <= s < expert_frequency_offset[e+1])
+ *   out[s,:] = a[row(s),:] W_e^T,   row(s) = x_gather_idx[s] if gather, else s.
+ * a [N,K] (gather) or [capacity,K] e4m3, a_scale [rows, ceil(K/128)]; w [E,C,K] e4m3,
+ * w_scale [E, ceil(C/128), ceil(K/128)]; out [capacity,C] bf16. Sums are fp32, but for
+ * what the matrix cores do with 8-bit operands: of eight products next to each other along
+ * K, each is cut off 2^13 below the largest one's power of two before they are added (with
+ * operands rounded from normal values about 1.6e-5 of the result, 1/100 of the rounding to
+ * bf16; nothing where the values of a block of 8 span at most four powers of two). Rows of
+ * out at positions >= P are left as they were; if P > capacity nothing is written. K and C
+ * positive multiples of 16 up to 2^20 (C: 2^21). */
+moe_status moe_grouped_gemm_fp8(const moe_metadata *meta, const void *a, const void *a_scale,
+                                moe_scale_type a_scale_type, const void *w,
+                                const void *w_scale, moe_scale_type w_scale_type, int32_t K,
+                                int32_t C, int32_t gather, void *out, void *stream);
+
+/* moe_expert_forward on e4m3 operands: x [N,H] with x_scale [N, ceil(H/128)]; w_up
+ * [E,2I,H] (rows in the order `layout` gives W_up's columns) and w_down [E,H,I], each
+ * row a column of moe_expert_forward's, with their block scales (both of w_scale_type).
+ *   h = x W_up_e^T;  a = silu(gate) * up, in e4m3 with a power-of-two scale per 128
+ *   values of a row;  y = a W_down_e^T;  out = sum of router_scores * y  (bf16).
+ * Sums as in moe_grouped_gemm_fp8; the 8-bit a is rounded from unrounded h; y is bf16. h_save
+ * [capacity,2I] bf16, interleaved, or NULL: moe_expert_backward takes it, with the bf16
+ * x and weights that the 8-bit ones stand for (the rounding to 8 bits taken as the
+ * identity). out is [N,H] bf16, 0 in rows with no valid slot, all 0 if P > capacity.
+ * H and I: positive multiples of 16, at most 2^20. */
+size_t moe_expert_forward_fp8_workspace(const moe_metadata *meta, int32_t H, int32_t I);
+moe_status moe_expert_forward_fp8(const moe_metadata *meta, const void *x, const void *x_scale,
+                                  moe_scale_type x_scale_type, const void *w_up,
+                                  const void *w_up_scale, const void *w_down,
+                                  const void *w_down_scale, moe_scale_type w_scale_type,
+                                  int32_t H, int32_t I, moe_gateup_layout layout,
+                                  void *h_save, void *out, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
 const char *moe_status_string(moe_status s);
 
 /* ---- Diagnostics: per-kernel timing with caller-created events ---------------
- * The kernels the three calls enqueue, in launch order. */
+ * The kernels the calls enqueue, in launch order. */
 typedef enum {
   MOE_KERNEL_META_HIST = 0,    /* moe_build_metadata: per-chunk expert histograms
                                   (above 2048 slots) */
@@ -208,7 +305,15 @@ typedef enum {
   MOE_KERNEL_ROUTE = 11,       /* moe_route: top-K, weights, histograms, P sums
                                   (then META_SCAN and META_SCATTER, which also form the
                                   load-balancing loss) */
-  MOE_KERNEL_COUNT = 12
+  MOE_KERNEL_QUANT_ROWS = 12,    /* moe_quantize_rows */
+  MOE_KERNEL_QUANT_WEIGHTS = 13, /* moe_quantize_weights */
+  MOE_KERNEL_RMSNORM = 14,       /* moe_rmsnorm_forward */
+  MOE_KERNEL_RMSNORM_BWD = 15,   /* moe_rmsnorm_backward: dx and partial sums of dweight */
+  MOE_KERNEL_RMSNORM_DW = 16,    /* moe_rmsnorm_backward: dweight */
+  MOE_KERNEL_GROUPED_FP8 = 17,   /* moe_grouped_gemm_fp8 */
+  MOE_KERNEL_UP_SWIGLU_FP8 = 18, /* moe_expert_forward_fp8: up-projection + SwiGLU, in 8 bits */
+  MOE_KERNEL_DOWN_FP8 = 19,      /* moe_expert_forward_fp8: down projection (then COMBINE) */
+  MOE_KERNEL_COUNT = 20
 } moe_kernel_id;
 
 /* After this call, the i-th launch of `kernel` (i < n_launches, counted from this

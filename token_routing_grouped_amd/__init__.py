@@ -12,4 +12,7 @@ from ._binding import (  # noqa: F401
     moe_expert_backward_workspace, moe_status_string, EXPORTED_SYMBOLS, KERNELS,
     moe_time_kernel, moe_kernel_name, moe_route, moe_route_workspace, MOE_ROUTE_SOFTMAX_TOPK,
     MOE_ROUTE_TOPK_SOFTMAX, moe_build_metadata_noalloc, MOE_NOALLOC_SCRATCH_BYTES,
+    MOE_SCALE_FP32, MOE_SCALE_E8M0, MOE_QBLOCK, moe_quantize_rows, moe_quantize_weights,
+    moe_rmsnorm_forward, moe_rmsnorm_backward, moe_rmsnorm_backward_workspace,
+    moe_grouped_gemm_fp8, moe_expert_forward_fp8, moe_expert_forward_fp8_workspace,
 )

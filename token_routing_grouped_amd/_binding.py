@@ -25,11 +25,18 @@ EXPORTED_SYMBOLS = [
     "moe_expert_backward_workspace", "moe_build_metadata", "moe_expert_forward",
     "moe_expert_backward", "moe_status_string", "moe_time_kernel", "moe_kernel_name",
     "moe_route_workspace", "moe_route", "moe_build_metadata_noalloc",
+    "moe_quantize_rows", "moe_quantize_weights", "moe_rmsnorm_forward",
+    "moe_rmsnorm_backward_workspace", "moe_rmsnorm_backward", "moe_grouped_gemm_fp8",
+    "moe_expert_forward_fp8_workspace", "moe_expert_forward_fp8",
 ]
 MOE_NOALLOC_SCRATCH_BYTES = 4 << 20
 KERNELS = ["meta_hist", "meta_scan", "meta_scatter", "up_swiglu", "down", "combine", "down_bwd",
-           "wgrad_down", "up_bwd", "wgrad_up", "combine_dx", "route"]
+           "wgrad_down", "up_bwd", "wgrad_up", "combine_dx", "route", "quant_rows",
+           "quant_weights", "rmsnorm", "rmsnorm_bwd", "rmsnorm_dw", "grouped_fp8",
+           "up_swiglu_fp8", "down_fp8"]
 MOE_ROUTE_SOFTMAX_TOPK, MOE_ROUTE_TOPK_SOFTMAX = 0, 1
+MOE_SCALE_FP32, MOE_SCALE_E8M0 = 0, 1
+MOE_QBLOCK = 128
 
 
 class MoeError(RuntimeError):
@@ -82,6 +89,24 @@ def lib():
         L.moe_route_workspace.argtypes = [i32, i32, i32]
         L.moe_route.restype = ctypes.c_int
         L.moe_route.argtypes = [vp, ctypes.c_int, ctypes.c_int, i32, vp, vp, vp, vp, vp, sz, vp]
+        ci, f32 = ctypes.c_int, ctypes.c_float
+        L.moe_quantize_rows.restype = ci
+        L.moe_quantize_rows.argtypes = [vp, i32, i32, ci, vp, vp, ci, vp]
+        L.moe_quantize_weights.restype = ci
+        L.moe_quantize_weights.argtypes = [vp, i32, i32, i32, ci, vp, vp, ci, vp]
+        L.moe_rmsnorm_forward.restype = ci
+        L.moe_rmsnorm_forward.argtypes = [vp, vp, vp, f32, i32, i32, ci, vp, vp, vp, vp, ci, vp, vp]
+        L.moe_rmsnorm_backward_workspace.restype = sz
+        L.moe_rmsnorm_backward_workspace.argtypes = [i32, i32]
+        L.moe_rmsnorm_backward.restype = ci
+        L.moe_rmsnorm_backward.argtypes = [vp, vp, vp, vp, vp, i32, i32, ci, vp, vp, vp, sz, vp]
+        L.moe_grouped_gemm_fp8.restype = ci
+        L.moe_grouped_gemm_fp8.argtypes = [vp, vp, vp, ci, vp, vp, ci, i32, i32, i32, vp, vp]
+        L.moe_expert_forward_fp8_workspace.restype = sz
+        L.moe_expert_forward_fp8_workspace.argtypes = [vp, i32, i32]
+        L.moe_expert_forward_fp8.restype = ci
+        L.moe_expert_forward_fp8.argtypes = [vp, vp, vp, ci, vp, vp, vp, vp, ci, i32, i32, ci, vp,
+                                             vp, vp, sz, vp]
         L.moe_time_kernel.restype = ctypes.c_int
         L.moe_time_kernel.argtypes = [ctypes.c_int, vp, i32, vp]
         L.moe_kernel_name.restype = ctypes.c_char_p
@@ -295,6 +320,203 @@ def moe_expert_backward(meta: Metadata, topk_idx, x, w_up, w_down, h_saved, dout
     with _on(meta, stream):
         _check(lib().moe_expert_backward(meta.ptr, *args, H, I, dt, layout, *outs, ws, nb,
                                          _stream(stream)), "moe_expert_backward")
+
+
+# ---- 8-bit operands ------------------------------------------------------------------
+
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _blocks(n: int) -> int:
+    return (n + MOE_QBLOCK - 1) // MOE_QBLOCK
+
+
+def _ptr(device, t, name: str, dtype, shape):
+    """Address of a contiguous tensor of this dtype and shape on `device` (as _dev_on checks
+    them, one attribute each: these calls are made per token in serving loops)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call on {device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _scale_code(t, name: str) -> int:
+    if isinstance(t, torch.Tensor):
+        if t.dtype is _E8M0:
+            return MOE_SCALE_E8M0
+        if t.dtype is torch.float32:
+            return MOE_SCALE_FP32
+    raise TypeError(f"{name} must be a float32 or float8_e8m0fnu tensor")
+
+
+def _first(t, name: str, dims: int):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
+    return t.device
+
+
+class _Device:
+    """Runs a call with `device` current (switched only when another one is); an explicit
+    stream must be on it. Gives the stream's handle."""
+
+    def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the call on {device}")
+        self.stream = stream
+        self.other = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
+
+    def __enter__(self):
+        if self.other is not None:
+            self.other.__enter__()
+        s = self.stream if self.stream is not None else torch.cuda.current_stream()
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.other is not None:
+            self.other.__exit__(*exc)
+
+
+def moe_quantize_rows(x, q, scale, stream=None):
+    """x [N,H] (bf16 or fp32) -> q [N,H] float8_e4m3fn, scale [N, ceil(H/128)] (float32 or
+    float8_e8m0fnu: powers of two either way)."""
+    dev = _first(x, "x", 2)
+    N, H = x.shape
+    px = _ptr(dev, x, "x", x.dtype, (N, H))
+    pq = _ptr(dev, q, "q", _E4M3, (N, H))
+    sc = _scale_code(scale, "scale")
+    ps = _ptr(dev, scale, "scale", scale.dtype, (N, _blocks(H)))
+    with _Device(dev, stream) as st:
+        _check(lib().moe_quantize_rows(px, N, H, _dtype_code(x), pq, ps, sc, st),
+               "moe_quantize_rows")
+
+
+def moe_quantize_weights(w, q, scale, stream=None):
+    """w [E,K,C] (bf16 or fp32, as moe_expert_forward takes W_up and W_down) -> q [E,C,K]
+    float8_e4m3fn, scale [E, ceil(C/128), ceil(K/128)] (float32 or float8_e8m0fnu)."""
+    dev = _first(w, "w", 3)
+    E, K, C = w.shape
+    pw = _ptr(dev, w, "w", w.dtype, (E, K, C))
+    pq = _ptr(dev, q, "q", _E4M3, (E, C, K))
+    sc = _scale_code(scale, "scale")
+    ps = _ptr(dev, scale, "scale", scale.dtype, (E, _blocks(C), _blocks(K)))
+    with _Device(dev, stream) as st:
+        _check(lib().moe_quantize_weights(pw, E, K, C, _dtype_code(w), pq, ps, sc, st),
+               "moe_quantize_weights")
+
+
+def moe_rmsnorm_forward(x, weight, eps: float = 1e-6, residual=None, residual_out=None, y=None,
+                        q=None, scale=None, rstd=None, stream=None):
+    """r = x + residual (to residual_out), y = r / sqrt(mean(r^2) + eps) * weight, to y (x's
+    dtype), to q and scale in 8 bits, or to both; rstd [N] fp32 for the backward. Every output
+    is passed in; residual_out may be x or residual itself."""
+    dev = _first(x, "x", 2)
+    dt = x.dtype
+    N, H = x.shape
+    px = _ptr(dev, x, "x", dt, (N, H))
+    pw = _ptr(dev, weight, "weight", dt, (H,))
+    pr = None if residual is None else _ptr(dev, residual, "residual", dt, (N, H))
+    po = None if residual_out is None else _ptr(dev, residual_out, "residual_out", dt, (N, H))
+    py = None if y is None else _ptr(dev, y, "y", dt, (N, H))
+    pq = None if q is None else _ptr(dev, q, "q", _E4M3, (N, H))
+    sc, ps = MOE_SCALE_FP32, None
+    if scale is not None:
+        sc = _scale_code(scale, "scale")
+        ps = _ptr(dev, scale, "scale", scale.dtype, (N, _blocks(H)))
+    pd = None if rstd is None else _ptr(dev, rstd, "rstd", torch.float32, (N,))
+    with _Device(dev, stream) as st:
+        _check(lib().moe_rmsnorm_forward(px, pr, pw, eps, N, H, _dtype_code(x), po, py, pq, ps, sc,
+                                         pd, st), "moe_rmsnorm_forward")
+
+
+def moe_rmsnorm_backward_workspace(N: int, H: int) -> int:
+    return int(lib().moe_rmsnorm_backward_workspace(N, H))
+
+
+def moe_rmsnorm_backward(dy, r, weight, rstd, dx, dweight, dresidual=None, workspace=None,
+                         stream=None):
+    """Gradients of moe_rmsnorm_forward: dx [N,H] (of x and of residual alike) and dweight [H]
+    from dy, the r and rstd that the forward left, and dresidual, residual_out's own gradient."""
+    dev = _first(r, "r", 2)
+    dt = r.dtype
+    N, H = r.shape
+    pr = _ptr(dev, r, "r", dt, (N, H))
+    pdy = _ptr(dev, dy, "dy", dt, (N, H))
+    pw = _ptr(dev, weight, "weight", dt, (H,))
+    ps = _ptr(dev, rstd, "rstd", torch.float32, (N,))
+    pz = None if dresidual is None else _ptr(dev, dresidual, "dresidual", dt, (N, H))
+    px = _ptr(dev, dx, "dx", dt, (N, H))
+    pdw = _ptr(dev, dweight, "dweight", dt, (H,))
+    with _Device(dev, stream) as st:
+        wst, ws, nb = _workspace(workspace, moe_rmsnorm_backward_workspace(N, H), dev, stream)
+        _check(lib().moe_rmsnorm_backward(pdy, pr, pw, ps, pz, N, H, _dtype_code(r), px, pdw, ws,
+                                          nb, st), "moe_rmsnorm_backward")
+
+
+def moe_grouped_gemm_fp8(meta: Metadata, a, a_scale, w, w_scale, out, gather: bool = True,
+                         stream=None):
+    """out[s,:] = a[x_gather_idx[s],:] W_e^T (gather; else a[s,:] W_e^T) for the sorted
+    positions s of each expert e. a [N,K] (gather) or [capacity,K] and w [E,C,K] are
+    float8_e4m3fn with scales [rows, ceil(K/128)] and [E, ceil(C/128), ceil(K/128)], each
+    float32 or float8_e8m0fnu; out [capacity,C] bf16, its rows at positions >= P left alone."""
+    dev = meta.device
+    if _first(w, "w", 3) != dev:
+        raise ValueError(f"w is on {w.device}, the call on {dev}")
+    E, C, K = w.shape
+    rows = meta.N if gather else meta.capacity
+    pa = _ptr(dev, a, "a", _E4M3, (rows, K))
+    ac = _scale_code(a_scale, "a_scale")
+    pas = _ptr(dev, a_scale, "a_scale", a_scale.dtype, (rows, _blocks(K)))
+    pw = _ptr(dev, w, "w", _E4M3, (meta.E, C, K))
+    wc = _scale_code(w_scale, "w_scale")
+    pws = _ptr(dev, w_scale, "w_scale", w_scale.dtype, (meta.E, _blocks(C), _blocks(K)))
+    po = _ptr(dev, out, "out", torch.bfloat16, (meta.capacity, C))
+    with _Device(dev, stream) as st:
+        _check(lib().moe_grouped_gemm_fp8(meta.ptr, pa, pas, ac, pw, pws, wc, K, C,
+                                          int(bool(gather)), po, st),
+               "moe_grouped_gemm_fp8")
+
+
+def moe_expert_forward_fp8_workspace(meta: Metadata, H: int, I: int) -> int:
+    return int(lib().moe_expert_forward_fp8_workspace(meta.ptr, H, I))
+
+
+def moe_expert_forward_fp8(meta: Metadata, x, x_scale, w_up, w_up_scale, w_down, w_down_scale, out,
+                           h_save=None, workspace=None, stream=None,
+                           layout: int = MOE_GATEUP_INTERLEAVED):
+    """moe_expert_forward on float8_e4m3fn operands with block scales: x [N,H], w_up [E,2I,H],
+    w_down [E,H,I]; scales float32 or float8_e8m0fnu (both weights' the same); out [N,H] and
+    h_save [capacity,2I] bf16."""
+    dev = meta.device
+    if _first(w_down, "w_down", 3) != dev:
+        raise ValueError(f"w_down is on {w_down.device}, the call on {dev}")
+    N, E = meta.N, meta.E
+    _, H, I = w_down.shape
+    px = _ptr(dev, x, "x", _E4M3, (N, H))
+    xc = _scale_code(x_scale, "x_scale")
+    pxs = _ptr(dev, x_scale, "x_scale", x_scale.dtype, (N, _blocks(H)))
+    pu = _ptr(dev, w_up, "w_up", _E4M3, (E, 2 * I, H))
+    wc = _scale_code(w_up_scale, "w_up_scale")
+    pus = _ptr(dev, w_up_scale, "w_up_scale", w_up_scale.dtype, (E, _blocks(2 * I), _blocks(H)))
+    pd = _ptr(dev, w_down, "w_down", _E4M3, (E, H, I))
+    pds = _ptr(dev, w_down_scale, "w_down_scale", w_up_scale.dtype, (E, _blocks(H), _blocks(I)))
+    po = _ptr(dev, out, "out", torch.bfloat16, (N, H))
+    ph = None if h_save is None else _ptr(dev, h_save, "h_save", torch.bfloat16,
+                                          (meta.capacity, 2 * I))
+    with _Device(dev, stream) as st:
+        wst, ws, nb = _workspace(workspace, moe_expert_forward_fp8_workspace(meta, H, I), dev,
+                                 stream)
+        _check(lib().moe_expert_forward_fp8(meta.ptr, px, pxs, xc, pu, pus, pd, pds, wc, H, I,
+                                            layout, ph, po, ws, nb, st),
+               "moe_expert_forward_fp8")
 
 
 def moe_kernel_name(kernel: int) -> str:

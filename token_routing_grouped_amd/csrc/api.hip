@@ -6,38 +6,15 @@
 #include <atomic>
 #include <mutex>
 
-#include "../../include/moe.h"
-#include "kernels.h"
+#include "api_common.h"
 
 using namespace moe;
 
+namespace moe {
+thread_local TimingHook g_hook;
+}
+
 namespace {
-
-constexpr size_t kAlign = 256;
-inline size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-inline size_t elem_size(moe_dtype dt) { return dt == MOE_BF16 ? 2 : 4; }
-
-bool meta_ok(const moe_metadata *m) {
-  if (!m) return false;
-  if (m->N < 0 || m->K < 1 || m->K > MOE_MAX_TOPK || m->E < 1 || m->E > MOE_MAX_EXPERTS)
-    return false;
-  const int64_t NK = (int64_t)m->N * m->K;
-  if (NK >= INT32_MAX) return false;
-  if (m->capacity < 0) return false;
-  if (!m->expert_frequency || !m->expert_frequency_offset ||
-      !m->num_activated_expert_per_token_offset || !m->status)
-    return false;
-  if (m->capacity > 0 &&
-      (!m->x_gather_idx || !m->s_scatter_idx || !m->s_reverse_scatter_idx || !m->router_scores))
-    return false;
-  if ((int64_t)meta_blocks(NK) * (m->E + 1) >= INT32_MAX) return false;
-  return true;
-}
-
-// H and I in whole 16-byte bf16 chunks; the GEMM tiles at their edges may be partial
-bool dims_ok(int32_t H, int32_t I) {
-  return H > 0 && I > 0 && H % 8 == 0 && I % 8 == 0 && H <= (1 << 20) && I <= (1 << 20);
-}
 
 struct FwdWs {
   size_t a, y, total;
@@ -63,32 +40,6 @@ BwdWs bwd_layout(const moe_metadata *m, int32_t H, int32_t I, moe_dtype dt) {
   w.total = w.partial + align_up(cap * (size_t)((I + kGemmBN - 1) / kGemmBN) * sizeof(float));
   return w;
 }
-
-// ---- diagnostics: events around the launches of one kernel. The hook belongs to the
-// host thread that armed it (thread-local): launches made by other threads never read
-// or advance it, so arming it in one thread cannot race with another thread's calls.
-struct TimingHook {
-  int kernel = -1;
-  hipEvent_t const *events = nullptr;
-  int n = 0, i = 0;
-};
-thread_local TimingHook g_hook;
-
-struct Bracket {  // records the start event on construction, the end event on destruction
-  hipStream_t st;
-  bool on;
-  int slot;
-  Bracket(moe_kernel_id k, hipStream_t s) : st(s), on(false), slot(0) {
-    if (g_hook.events && g_hook.kernel == (int)k && g_hook.i < g_hook.n) {
-      on = true;
-      slot = g_hook.i++;
-      (void)hipEventRecord(g_hook.events[2 * slot], st);
-    }
-  }
-  ~Bracket() {
-    if (on) (void)hipEventRecord(g_hook.events[2 * slot + 1], st);
-  }
-};
 
 GemmArgs base_args(const moe_metadata *m) {
   GemmArgs g = {};
@@ -441,7 +392,8 @@ moe_status moe_time_kernel(moe_kernel_id kernel, void *const *events, int32_t n_
 const char *moe_kernel_name(moe_kernel_id k) {
   static const char *names[MOE_KERNEL_COUNT] = {
       "meta_hist", "meta_scan", "meta_scatter", "up_swiglu", "down", "combine", "down_bwd",
-      "wgrad_down", "up_bwd", "wgrad_up", "combine_dx", "route"};
+      "wgrad_down", "up_bwd", "wgrad_up", "combine_dx", "route", "quant_rows", "quant_weights",
+      "rmsnorm", "rmsnorm_bwd", "rmsnorm_dw", "grouped_fp8", "up_swiglu_fp8", "down_fp8"};
   return ((int)k >= 0 && (int)k < MOE_KERNEL_COUNT) ? names[(int)k] : "unknown";
 }
 

@@ -1,0 +1,321 @@
+// Grouped products over e4m3 operands with a scale per block of 128, on gfx950 matrix cores.
+//
+//   out[s,:] = sum over the blocks b of K of  (a_s,b . w_n,b) sa[s,b] sw[n/128,b]
+//
+// for the sorted positions s of each expert's segment. Sums are fp32, but that the matrix
+// cores cut each of eight products next to each other along K off 2^13 below the largest
+// one's power of two (measured, in-bounds, at every position of a block; the 32-wide fp8
+// instructions of the same rate as bf16's do the same): about 1.6e-5 of a result of rounded
+// normal values, against 1.7e-3 for the outputs' bf16. Taken for twice the rate of bf16
+// products, the only exact way. A tile is BT tokens x BN
+// output columns; a workgroup finds its tile from the segment offsets, as the bf16 products
+// do. One v_mfma_f32_16x16x128_f8f6f4 covers exactly one block of the reduction. The weights
+// are its first operand, so a lane holds four consecutive output columns of one token: one
+// token scale per lane, and (gate, up) pairs side by side.
+//
+// Scales that are powers of two (e8m0) go into the matrix instruction, which multiplies each
+// operand row's products by them for nothing; fp32 scales multiply the block's sums.
+//
+// LDS holds two stages of BT + BN rows of 128 bytes, filled by direct global-to-LDS loads one
+// block ahead. The 16-byte chunk c of row r lies at chunk c ^ ((r / 2) % 8), so the 16 rows
+// that a fragment read takes at one chunk cover all 64 banks once. Chunks past K, whole in
+// both operands, come from a page of zeros; rows past the segment repeat its first row and
+// are never stored.
+#include "../../include/moe.h"
+#include "fp8.h"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __attribute__((aligned(128))) uint32_t g_zeros[32];  // starts zeroed, never written
+
+// 16 bytes per lane from global memory to LDS: lane l's go to lds + 16 l. The wait for it is
+// wait_loads().
+__device__ __forceinline__ void load_to_lds(const void *p, void *lds) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)p,
+                                   (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ float scale_value(const void *p, int e8m0, int64_t i) {
+  return e8m0 ? exponent_value(((const uint8_t *)p)[i]) : ((const float *)p)[i];
+}
+
+constexpr int kKC = 8;  // blocks of K whose scales LDS holds at a time (two such sets)
+
+// WT x WN waves; HW: both scales are e8m0
+template <bool HW, bool SWI, int BT, int BN, int WT, int WN>
+__global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
+  constexpr int NT = 64 * WT * WN, NW = WT * WN;
+  constexpr int TT = BT / WT / 16, TN = BN / WN / 16;  // 16 x 16 pieces of a wave
+  constexpr int ROWS = BT + BN, STAGE = ROWS * kQB;
+  constexpr int LD = ROWS / 8 / NW;  // 1 KB loads per wave and stage
+  static_assert(ROWS % (8 * NW) == 0 && BT % 8 == 0, "whole loads");
+  static_assert(!SWI || BN == 256, "a SwiGLU tile holds one block of 128 pairs");
+  constexpr int F = BN / 16;                     // column pieces of the tile
+  __shared__ __attribute__((aligned(128))) uint8_t smem[2 * STAGE];
+  __shared__ uint32_t s_sa[2][kKC][BT];          // token scales (bits: e8m0 byte or fp32)
+  __shared__ uint32_t s_sw[2][kKC][F][2];        // weight scales of a piece's even and odd rows
+  __shared__ int s_tab[2 * (MOE_MAX_EXPERTS + 1)];
+  int *s_pref = s_tab, *s_off = s_tab + MOE_MAX_EXPERTS + 1;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wt = wave / WN, wn = wave % WN;
+  const int P = g.foff[g.E];
+  if (P > g.cap) return;
+  for (int i = tid; i <= g.E; i += NT) {
+    const int o = g.foff[i];
+    s_off[i] = o;
+    if (i < g.E) s_pref[i] = (g.foff[i + 1] - o + BT - 1) / BT;
+  }
+  __syncthreads();
+  wave0_exclusive_scan(s_pref, g.E);
+  __syncthreads();
+  const int ntn = (g.C + BN - 1) / BN;
+  const int64_t G = (int64_t)s_pref[g.E] * ntn;
+  // XCD x (= blockIdx % 8) owns one contiguous run of the tiles
+  int64_t L;
+  {
+    const int x = blockIdx.x % kNumXcd;
+    const int64_t i = blockIdx.x / kNumXcd, q = G / kNumXcd;
+    const int rq = (int)(G % kNumXcd);
+    if (i >= q + (x < rq ? 1 : 0)) return;
+    L = x * q + (x < rq ? x : rq) + i;
+  }
+  const int mtile = (int)(L / ntn), nt = (int)(L - (int64_t)mtile * ntn);
+  int lo = 0, hi = g.E - 1;  // largest e with s_pref[e] <= mtile
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s_pref[mid] <= mtile) lo = mid; else hi = mid - 1;
+  }
+  const int e = __builtin_amdgcn_readfirstlane(lo);
+  const int row0 = __builtin_amdgcn_readfirstlane(s_off[lo] + (mtile - s_pref[lo]) * BT);
+  const int rows = __builtin_amdgcn_readfirstlane(min(BT, s_off[lo + 1] - row0));
+  const int nk = g.nbk, I = g.C >> 1;
+
+  // memory row of tile column n: the columns of a SwiGLU tile are (gate, up) pairs in order
+  auto w_row = [&](int n) {
+    int c = nt * BN + n;
+    c = c < g.C ? c : g.C - 1;
+    return SWI && g.concat ? (c & 1 ? I : 0) + (c >> 1) : c;
+  };
+  // ---- this lane's rows of a stage: row (wave + NW i) * 8 + lane / 8, and its chunk there
+  const uint8_t *ptr[LD];
+  int ck[LD];  // chunk's offset in the block
+#pragma unroll
+  for (int i = 0; i < LD; i++) {
+    const int r = (wave + NW * i) * 8 + (lane >> 3);
+    ck[i] = ((lane & 7) ^ ((r >> 1) & 7)) * 16;
+    if (r < BT) {
+      const int s = row0 + (r < rows ? r : 0);
+      const int64_t m = g.a_rows ? g.a_rows[s] : s;
+      ptr[i] = g.a + m * g.K + ck[i];
+    } else {
+      ptr[i] = g.w + ((int64_t)e * g.C + w_row(r - BT)) * g.K + ck[i];
+    }
+  }
+  auto issue = [&](int kb) {
+    uint8_t *st = smem + (kb & 1) * STAGE;
+    const int k0 = kb * kQB;
+#pragma unroll
+    for (int i = 0; i < LD; i++) {
+      const void *p = k0 + ck[i] < g.K ? (const void *)(ptr[i] + k0)
+                                       : (const void *)((const uint8_t *)g_zeros + ck[i]);
+      load_to_lds(p, st + (wave + NW * i) * 1024);
+    }
+  };
+  // ---- scales of blocks kb .. kb + 7 into set (kb / 8) % 2
+  auto put_scales = [&](int kb) {
+    const int set = (kb / kKC) & 1;
+    for (int i = tid; i < kKC * BT; i += NT) {
+      const int r = i / kKC, k = i % kKC, s = row0 + (r < rows ? r : 0);
+      const int64_t m = g.a_rows ? g.a_rows[s] : s;
+      const int64_t at = m * g.nbk + min(kb + k, nk - 1);
+      s_sa[set][k][r] = HW ? (uint32_t)((const uint8_t *)g.a_scale)[at]
+                           : __float_as_uint(scale_value(g.a_scale, g.a_e8m0, at));
+    }
+    for (int i = tid; i < kKC * F * 2; i += NT) {
+      const int k = i / (F * 2), f = (i >> 1) % F, odd = i & 1;
+      const int64_t at = ((int64_t)e * g.nbc + w_row(f * 16 + odd) / kQB) * g.nbk + min(kb + k, nk - 1);
+      s_sw[set][k][f][odd] = HW ? (uint32_t)((const uint8_t *)g.w_scale)[at]
+                                : __float_as_uint(scale_value(g.w_scale, g.w_e8m0, at));
+    }
+  };
+
+  f32x4 acc[TN][TT];
+#pragma unroll
+  for (int n = 0; n < TN; n++)
+#pragma unroll
+    for (int t = 0; t < TT; t++) acc[n][t] = f32x4{0, 0, 0, 0};
+
+  // operand of 16 rows from row r0 of a stage: lane l takes 32 bytes of row r0 + l % 16
+  const int fr = lane & 15, fg = lane >> 4;
+  auto frag = [&](const uint8_t *st, int r0) {
+    const int r = r0 + fr, sw = (r >> 1) & 7;
+    const uint8_t *p = st + r * kQB;
+    const i32x4 a = *(const i32x4 *)(p + (((2 * fg) ^ sw) << 4));
+    const i32x4 b = *(const i32x4 *)(p + (((2 * fg + 1) ^ sw) << 4));
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+
+  issue(0);
+  put_scales(0);
+  for (int kb = 0; kb < nk; kb++) {
+    wait_loads();
+    __syncthreads();  // stage kb is there, and everyone is done with stage kb - 1
+    if (kb + 1 < nk) issue(kb + 1);
+    if (kb % kKC == 0 && kb + kKC < nk) put_scales(kb + kKC);
+    const uint8_t *st = smem + (kb & 1) * STAGE;
+    const int set = (kb / kKC) & 1, k = kb % kKC;
+    i32x8 bt[TT];
+    uint32_t sa[TT];
+#pragma unroll
+    for (int t = 0; t < TT; t++) {
+      const int r = wt * (BT / WT) + t * 16;
+      bt[t] = frag(st, r);
+      sa[t] = s_sa[set][k][r + fr];
+    }
+#pragma unroll
+    for (int n = 0; n < TN; n++) {
+      const int c = wn * (BN / WN) + n * 16;
+      const i32x8 an = frag(st, BT + c);
+      const uint32_t *sw = s_sw[set][k][c / 16];
+      if constexpr (HW) {
+        const uint32_t sn = sw[fr & 1];
+#pragma unroll
+        for (int t = 0; t < TT; t++)
+          acc[n][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(an, bt[t], acc[n][t], 0, 0, 0,
+                                                                       (int)sn, 0, (int)sa[t]);
+      } else {
+        const float se = __uint_as_float(sw[0]), so = __uint_as_float(sw[1]);
+#pragma unroll
+        for (int t = 0; t < TT; t++) {
+          const f32x4 z = {0, 0, 0, 0};
+          const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              an, bt[t], z, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+          const float x0 = __uint_as_float(sa[t]) * se, x1 = __uint_as_float(sa[t]) * so;
+          acc[n][t][0] += d[0] * x0;
+          acc[n][t][1] += d[1] * x1;
+          acc[n][t][2] += d[2] * x0;
+          acc[n][t][3] += d[3] * x1;
+        }
+      }
+    }
+  }
+
+  // The sums are pinned here: a matrix instruction moved under a later per-lane condition
+  // would take its operands from loads that only the condition's lanes make.
+#pragma unroll
+  for (int n = 0; n < TN; n++)
+#pragma unroll
+    for (int t = 0; t < TT; t++) asm volatile("" : "+v"(acc[n][t]));
+
+  // ---- epilogues: acc[n][t] of lane l holds columns cb .. cb + 3 of token tok
+  if constexpr (!SWI) {
+#pragma unroll
+    for (int t = 0; t < TT; t++) {
+      const int tok = wt * (BT / WT) + t * 16 + fr;
+      if (tok >= rows) continue;
+      const int64_t o = (int64_t)(row0 + tok) * g.C;
+#pragma unroll
+      for (int n = 0; n < TN; n++) {
+        const int c = nt * BN + wn * (BN / WN) + n * 16 + fg * 4;
+        if (c >= g.C) continue;
+        const f32x4 v = acc[n][t];
+        *(u32x2 *)(g.out + o + c) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      }
+    }
+  } else {
+    // a = silu(gate) up; the block of 128 is the whole tile, so a token's maximum is taken
+    // over the four lanes that share it and over the WN waves
+    float av[TN][TT][2];
+    __syncthreads();  // everyone is done with the stages
+    uint32_t *red = (uint32_t *)smem;  // [WN][BT]
+    uint8_t *sq = smem + WN * BT * 4;  // [BT][128 + 16]
+    constexpr int QLD = kQB + 16;
+    static_assert(WN * BT * 4 + BT * QLD <= 2 * STAGE, "epilogue fits the stages");
+#pragma unroll
+    for (int t = 0; t < TT; t++) {
+      const int tok = wt * (BT / WT) + t * 16 + fr;
+      const int64_t o = (int64_t)(row0 + tok) * g.C;
+      uint32_t m = 0;
+#pragma unroll
+      for (int n = 0; n < TN; n++) {
+        const int c = nt * BN + wn * (BN / WN) + n * 16 + fg * 4;
+        const bool in = c < g.C;
+        const f32x4 v = acc[n][t];
+        if (g.out && in && tok < rows)
+          *(u32x2 *)(g.out + o + c) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+#pragma unroll
+        for (int p = 0; p < 2; p++) {
+          av[n][t][p] = in ? silu_f(v[2 * p]) * v[2 * p + 1] : 0.0f;
+          const uint32_t b = finite_abs_bits(av[n][t][p]);
+          m = m > b ? m : b;
+        }
+      }
+#pragma unroll
+      for (int s = 16; s < 64; s <<= 1) {
+        const uint32_t u = (uint32_t)__shfl_xor((int)m, s, kWave);
+        m = m > u ? m : u;
+      }
+      if (fg == 0) red[wn * BT + tok] = m;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < TT; t++) {
+      const int tok = wt * (BT / WT) + t * 16 + fr;
+      uint32_t m = red[tok];
+#pragma unroll
+      for (int w = 1; w < WN; w++) m = m > red[w * BT + tok] ? m : red[w * BT + tok];
+      const uint32_t ex = scale_exponent(m);
+      const float inv = exponent_inverse(ex);
+#pragma unroll
+      for (int n = 0; n < TN; n++) {
+        const uint32_t q = pack_e4m3(to_q(av[n][t][0], inv), to_q(av[n][t][1], inv), 0.0f, 0.0f);
+        *(uint16_t *)(sq + tok * QLD + (wn * (BN / WN) + n * 16 + fg * 4) / 2) = (uint16_t)q;
+      }
+      if (wn == 0 && fg == 0 && tok < rows)
+        g.aq_scale[(int64_t)(row0 + tok) * ((I + kQB - 1) / kQB) + nt] = (uint8_t)ex;
+    }
+    __syncthreads();
+    for (int i = tid; i < BT * 8; i += NT) {
+      const int tok = i >> 3, ch = (i & 7) * 16, j = nt * kQB + ch;
+      if (tok < rows && j < I)
+        *(u32x4 *)(g.aq + (int64_t)(row0 + tok) * I + j) = *(const u32x4 *)(sq + tok * QLD + ch);
+    }
+  }
+}
+
+constexpr int kBT = 128, kBN = 256;
+
+template <bool HW, bool SWI>
+hipError_t go(const Fp8Args &g, int grid, hipStream_t st) {
+  hipLaunchKernelGGL((gemm_fp8_kernel<HW, SWI, kBT, kBN, 2, 4>), dim3(grid), dim3(512), 0, st, g);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// Workgroups: row tiles of every segment, bounded from the capacity, times column tiles, in
+// whole rounds of the XCDs; fewer than 2^32 lanes in a launch.
+int64_t fp8_grid(bool swiglu, const Fp8Args &g) {
+  const int64_t mt = ((int64_t)g.cap + (int64_t)g.E * (kBT - 1)) / kBT;
+  const int64_t grid = (mt * ((g.C + kBN - 1) / kBN) + kNumXcd - 1) / kNumXcd * kNumXcd;
+  return grid > (1 << 23) - kNumXcd ? -1 : grid;
+}
+
+hipError_t launch_gemm_fp8(bool swiglu, const Fp8Args &g, hipStream_t st) {
+  const int64_t grid = fp8_grid(swiglu, g);
+  if (grid < 0) return hipErrorInvalidValue;
+  if (grid == 0) return hipSuccess;
+  const bool hw = g.a_e8m0 && g.w_e8m0;
+  if (swiglu) return hw ? go<true, true>(g, (int)grid, st) : go<false, true>(g, (int)grid, st);
+  return hw ? go<true, false>(g, (int)grid, st) : go<false, false>(g, (int)grid, st);
+}
+
+}  // namespace moe

@@ -158,4 +158,47 @@ hipError_t launch_combine_dscore(bool bf16, const void *dxg, const int32_t *tok_
                                  const int32_t *topk_idx, int K, int E, const float *partial,
                                  int n_ntiles, float *d_topk_weights, hipStream_t stream);
 
+// ---- 8-bit operands -----------------------------------------------------------
+// Rows and weights in e4m3 with power-of-two scales (fp32, or the exponent's byte).
+hipError_t launch_quantize_rows(const void *x, int N, int H, bool bf16, void *q, void *scale,
+                                int e8m0, hipStream_t st);
+hipError_t launch_quantize_weights(const void *w, int E, int K, int C, bool bf16, void *q,
+                                   void *scale, int e8m0, hipStream_t st);
+
+// RMS norm; the backward's shares of dweight ([shares][H] fp32) are added by the second
+// launch.
+hipError_t launch_rmsnorm(const void *x, const void *residual, const void *weight, float eps, int N,
+                          int H, bool bf16, void *r, void *y, void *q, void *scale, int e8m0,
+                          float *rstd, hipStream_t st);
+inline int rmsnorm_shares(int N, int H) {
+  const int most = H <= 16384 ? 512 : 64;
+  return N < most ? N : most;
+}
+hipError_t launch_rmsnorm_bwd(const void *dy, const void *r, const void *weight, const float *rstd,
+                              const void *dres, int N, int H, bool bf16, void *dx, float *part,
+                              hipStream_t st);
+hipError_t launch_rmsnorm_dw(const float *part, int N, int H, bool bf16, void *dw, hipStream_t st);
+
+// Grouped products: out[s,:] = a[row(s),:] W_e^T over e4m3 operands, both [.., K]
+// reduction-contiguous, with a scale per row and 128 (a) and per 128 x 128 (w).
+struct Fp8Args {
+  const int32_t *foff;  // [E+1]
+  int E, cap;
+  int C, K;  // output columns and reduction length
+  const uint8_t *a;
+  const int32_t *a_rows;  // row map (gather) or null = identity
+  const void *a_scale;
+  const uint8_t *w;
+  const void *w_scale;
+  int a_e8m0, w_e8m0;
+  int nbk, nbc;  // blocks along K and C
+  uint16_t *out;  // bf16 [cap,C]; SwiGLU: h_save, or null
+  // SwiGLU: C = 2I; a = silu(gate) up in e4m3 [cap,I] with e8m0 scales [cap, ceil(I/128)]
+  uint8_t *aq;
+  uint8_t *aq_scale;
+  int concat;  // rows of w (and its scale blocks) are [gates | ups]
+};
+int64_t fp8_grid(bool swiglu, const Fp8Args &g);  // -1: too large
+hipError_t launch_gemm_fp8(bool swiglu, const Fp8Args &g, hipStream_t st);
+
 }  // namespace moe
