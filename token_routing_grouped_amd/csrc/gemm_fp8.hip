@@ -33,13 +33,21 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __attribute__((aligned(128))) uint32_t g_zeros[32];  // starts zeroed, never written
 
-// 16 bytes per lane from global memory to LDS: lane l's go to lds + 16 l. The wait for it is
-// wait_loads().
-__device__ __forceinline__ void load_to_lds(const void *p, void *lds) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)p,
-                                   (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
+// 16 bytes per lane from global memory to LDS: lane l's go to lds + 16 l. Written as asm so
+// that the compiler does not make every later LDS read wait for it (it cannot tell the two
+// stages apart); nothing is returned in registers, and the wait is wait_loads(), ahead of
+// the barrier that hands the stage over.
+__device__ __forceinline__ void load_to_lds(const void *p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(lds), "v"(p)
+               : "memory");
 }
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+  return (uint32_t)__builtin_amdgcn_readfirstlane(
+      (int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p);
+}
 
 __device__ __forceinline__ float scale_value(const void *p, int e8m0, int64_t i) {
   return e8m0 ? exponent_value(((const uint8_t *)p)[i]) : ((const float *)p)[i];
@@ -49,14 +57,16 @@ constexpr int kKC = 8;  // blocks of K whose scales LDS holds at a time (two suc
 
 // WT x WN waves; HW: both scales are e8m0
 template <bool HW, bool SWI, int BT, int BN, int WT, int WN>
-__global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
+__global__ __launch_bounds__(64 * WT * WN, WT *WN == 8 ? 2 : 1) void gemm_fp8_kernel(Fp8Args g) {
   constexpr int NT = 64 * WT * WN, NW = WT * WN;
   constexpr int TT = BT / WT / 16, TN = BN / WN / 16;  // 16 x 16 pieces of a wave
   constexpr int ROWS = BT + BN, STAGE = ROWS * kQB;
   constexpr int LD = ROWS / 8 / NW;  // 1 KB loads per wave and stage
-  static_assert(ROWS % (8 * NW) == 0 && BT % 8 == 0, "whole loads");
+  static_assert(ROWS % (8 * NW) == 0 && BT % (8 * NW) == 0, "a load is of one operand");
   static_assert(!SWI || BN == 256, "a SwiGLU tile holds one block of 128 pairs");
   constexpr int F = BN / 16;                     // column pieces of the tile
+  constexpr int SA = kKC * BT / NT, SW = (kKC * F * 2 + NT - 1) / NT;  // scales per thread
+  static_assert(kKC * BT % NT == 0 && NT % BT == 0, "whole rounds");
   __shared__ __attribute__((aligned(128))) uint8_t smem[2 * STAGE];
   __shared__ uint32_t s_sa[2][kKC][BT];          // token scales (bits: e8m0 byte or fp32)
   __shared__ uint32_t s_sw[2][kKC][F][2];        // weight scales of a piece's even and odd rows
@@ -76,135 +86,171 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   __syncthreads();
   wave0_exclusive_scan(s_pref, g.E);
   __syncthreads();
+  // Persistent workgroups: XCD x (= blockIdx % 8) owns one contiguous run of the tiles, which
+  // its workgroups take in turn
   const int ntn = (g.C + BN - 1) / BN;
   const int64_t G = (int64_t)s_pref[g.E] * ntn;
-  // XCD x (= blockIdx % 8) owns one contiguous run of the tiles
-  int64_t L;
-  {
-    const int x = blockIdx.x % kNumXcd;
-    const int64_t i = blockIdx.x / kNumXcd, q = G / kNumXcd;
-    const int rq = (int)(G % kNumXcd);
-    if (i >= q + (x < rq ? 1 : 0)) return;
-    L = x * q + (x < rq ? x : rq) + i;
-  }
-  const int mtile = (int)(L / ntn), nt = (int)(L - (int64_t)mtile * ntn);
-  int lo = 0, hi = g.E - 1;  // largest e with s_pref[e] <= mtile
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (s_pref[mid] <= mtile) lo = mid; else hi = mid - 1;
-  }
-  const int e = __builtin_amdgcn_readfirstlane(lo);
-  const int row0 = __builtin_amdgcn_readfirstlane(s_off[lo] + (mtile - s_pref[lo]) * BT);
-  const int rows = __builtin_amdgcn_readfirstlane(min(BT, s_off[lo + 1] - row0));
+  const int x = blockIdx.x % kNumXcd;
+  const int64_t gq = G / kNumXcd;
+  const int gr = (int)(G % kNumXcd);
+  const int64_t tend = (x + 1) * gq + min(x + 1, gr);
+  int64_t L = x * gq + min(x, gr) + blockIdx.x / kNumXcd;
   const int nk = g.nbk, I = g.C >> 1;
+  const uint32_t lds0 = lds_address(smem);
 
-  // memory row of tile column n: the columns of a SwiGLU tile are (gate, up) pairs in order
-  auto w_row = [&](int n) {
+  // ---- a tile: its expert, first row, rows and column tile; the rows of a stage that this
+  // lane loads, (wave + NW i) * 8 + lane / 8, and its chunk there; the scales it fetches
+  int e, nt, row0, rows;
+  const uint8_t *ptr[LD];
+  const int cs = (lane & 7) ^ ((lane >> 4) | ((wave & 1) << 2));  // chunk of every row of this lane
+  const int ck = cs * 16;
+  int64_t sa_row = 0;
+  auto w_row = [&](int n) {  // memory row of tile column n: SwiGLU tiles hold (gate, up) pairs
     int c = nt * BN + n;
     c = c < g.C ? c : g.C - 1;
     return SWI && g.concat ? (c & 1 ? I : 0) + (c >> 1) : c;
   };
-  // ---- this lane's rows of a stage: row (wave + NW i) * 8 + lane / 8, and its chunk there
-  const uint8_t *ptr[LD];
-  int ck[LD];  // chunk's offset in the block
-#pragma unroll
-  for (int i = 0; i < LD; i++) {
-    const int r = (wave + NW * i) * 8 + (lane >> 3);
-    ck[i] = ((lane & 7) ^ ((r >> 1) & 7)) * 16;
-    if (r < BT) {
-      const int s = row0 + (r < rows ? r : 0);
-      const int64_t m = g.a_rows ? g.a_rows[s] : s;
-      ptr[i] = g.a + m * g.K + ck[i];
-    } else {
-      ptr[i] = g.w + ((int64_t)e * g.C + w_row(r - BT)) * g.K + ck[i];
+  auto set_tile = [&](int64_t l_) {
+    // within an expert, groups of four row tiles, column tiles outer: the tiles that an XCD
+    // works on at a time then share their rows as well as their weights
+    int lo = 0, hi = g.E - 1;  // largest e with s_pref[e] * ntn <= l_
+    const int mtile = (int)(l_ / ntn);
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_pref[mid] <= mtile) lo = mid; else hi = mid - 1;
     }
-  }
-  auto issue = [&](int kb) {
-    uint8_t *st = smem + (kb & 1) * STAGE;
-    const int k0 = kb * kQB;
+    e = __builtin_amdgcn_readfirstlane(lo);
+    const int mte = s_pref[lo + 1] - s_pref[lo];
+    const int l = (int)(l_ - (int64_t)s_pref[lo] * ntn);
+    constexpr int GM = 4;
+    const int gi = l / (GM * ntn), rem = l - gi * GM * ntn, gm = min(GM, mte - gi * GM);
+    nt = __builtin_amdgcn_readfirstlane(rem / gm);
+    const int mt = gi * GM + rem - rem / gm * gm;
+    row0 = __builtin_amdgcn_readfirstlane(s_off[lo] + mt * BT);
+    rows = __builtin_amdgcn_readfirstlane(min(BT, s_off[lo + 1] - row0));
 #pragma unroll
     for (int i = 0; i < LD; i++) {
-      const void *p = k0 + ck[i] < g.K ? (const void *)(ptr[i] + k0)
-                                       : (const void *)((const uint8_t *)g_zeros + ck[i]);
-      load_to_lds(p, st + (wave + NW * i) * 1024);
+      const int r = (wave + NW * i) * 8 + (lane >> 3);
+      if (NW * i * 8 < BT) {
+        const int s = row0 + (r < rows ? r : 0);
+        const int64_t m = g.a_rows ? g.a_rows[s] : s;
+        ptr[i] = g.a + m * g.K + ck;
+      } else {
+        ptr[i] = g.w + ((int64_t)e * g.C + w_row(r - BT)) * g.K + ck;
+      }
+    }
+    const int r = tid % BT, s = row0 + (r < rows ? r : 0);
+    sa_row = (g.a_rows ? (int64_t)g.a_rows[s] : s) * g.nbk;
+  };
+  auto issue = [&](int kb) {
+    const uint32_t st = lds0 + (kb & 1) * STAGE + wave * 1024;
+    const int k0 = kb * kQB;
+    const bool in = k0 + ck < g.K;
+#pragma unroll
+    for (int i = 0; i < LD; i++)
+      load_to_lds(in ? (const void *)(ptr[i] + k0) : (const void *)((const uint8_t *)g_zeros + ck),
+                  st + NW * i * 1024);
+  };
+  // ---- scales of kKC blocks from kb: fetched into registers, put into LDS later
+  uint32_t ra[SA], rw[SW];
+  auto get_scales = [&](int kb) {
+#pragma unroll
+    for (int i = 0; i < SA; i++) {
+      const int64_t at = sa_row + min(kb + tid / BT + i * (NT / BT), nk - 1);
+      ra[i] = HW ? (uint32_t)((const uint8_t *)g.a_scale)[at]
+                 : __float_as_uint(scale_value(g.a_scale, g.a_e8m0, at));
+    }
+#pragma unroll
+    for (int i = 0; i < SW; i++) {
+      const int j = min(tid + NT * i, kKC * F * 2 - 1);
+      const int k = j / (F * 2), f = (j >> 1) % F, odd = j & 1;
+      const int64_t at = ((int64_t)e * g.nbc + w_row(f * 16 + odd) / kQB) * g.nbk + min(kb + k, nk - 1);
+      rw[i] = HW ? (uint32_t)((const uint8_t *)g.w_scale)[at]
+                 : __float_as_uint(scale_value(g.w_scale, g.w_e8m0, at));
     }
   };
-  // ---- scales of blocks kb .. kb + 7 into set (kb / 8) % 2
   auto put_scales = [&](int kb) {
     const int set = (kb / kKC) & 1;
-    for (int i = tid; i < kKC * BT; i += NT) {
-      const int r = i / kKC, k = i % kKC, s = row0 + (r < rows ? r : 0);
-      const int64_t m = g.a_rows ? g.a_rows[s] : s;
-      const int64_t at = m * g.nbk + min(kb + k, nk - 1);
-      s_sa[set][k][r] = HW ? (uint32_t)((const uint8_t *)g.a_scale)[at]
-                           : __float_as_uint(scale_value(g.a_scale, g.a_e8m0, at));
-    }
-    for (int i = tid; i < kKC * F * 2; i += NT) {
-      const int k = i / (F * 2), f = (i >> 1) % F, odd = i & 1;
-      const int64_t at = ((int64_t)e * g.nbc + w_row(f * 16 + odd) / kQB) * g.nbk + min(kb + k, nk - 1);
-      s_sw[set][k][f][odd] = HW ? (uint32_t)((const uint8_t *)g.w_scale)[at]
-                                : __float_as_uint(scale_value(g.w_scale, g.w_e8m0, at));
+#pragma unroll
+    for (int i = 0; i < SA; i++) s_sa[set][tid / BT + i * (NT / BT)][tid % BT] = ra[i];
+#pragma unroll
+    for (int i = 0; i < SW; i++) {
+      const int j = tid + NT * i;
+      if (j < kKC * F * 2) (&s_sw[set][0][0][0])[j] = rw[i];
     }
   };
 
+  // operand of 16 rows from row r0 of a stage: lane l takes 32 bytes of row r0 + l % 16
+  const int fr = lane & 15, fg = lane >> 4;
+  const int fsw = (fr >> 1) & 7;
+  const int fo0 = fr * kQB + (((2 * fg) ^ fsw) << 4), fo1 = fr * kQB + (((2 * fg + 1) ^ fsw) << 4);
+  auto frag = [&](const uint8_t *st, int r0) {
+    const i32x4 a = *(const i32x4 *)(st + r0 * kQB + fo0);
+    const i32x4 b = *(const i32x4 *)(st + r0 * kQB + fo1);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+
+  for (; L < tend; L += gridDim.x / kNumXcd) {
+  set_tile(L);
   f32x4 acc[TN][TT];
 #pragma unroll
   for (int n = 0; n < TN; n++)
 #pragma unroll
     for (int t = 0; t < TT; t++) acc[n][t] = f32x4{0, 0, 0, 0};
-
-  // operand of 16 rows from row r0 of a stage: lane l takes 32 bytes of row r0 + l % 16
-  const int fr = lane & 15, fg = lane >> 4;
-  auto frag = [&](const uint8_t *st, int r0) {
-    const int r = r0 + fr, sw = (r >> 1) & 7;
-    const uint8_t *p = st + r * kQB;
-    const i32x4 a = *(const i32x4 *)(p + (((2 * fg) ^ sw) << 4));
-    const i32x4 b = *(const i32x4 *)(p + (((2 * fg + 1) ^ sw) << 4));
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  };
-
   issue(0);
+  get_scales(0);
   put_scales(0);
   for (int kb = 0; kb < nk; kb++) {
     wait_loads();
+    if (kb % kKC == kKC - 1 && kb + 1 < nk) put_scales(kb + 1);
     __syncthreads();  // stage kb is there, and everyone is done with stage kb - 1
     if (kb + 1 < nk) issue(kb + 1);
-    if (kb % kKC == 0 && kb + kKC < nk) put_scales(kb + kKC);
+    if (kb % kKC == 0 && kb + kKC < nk) get_scales(kb + kKC);
     const uint8_t *st = smem + (kb & 1) * STAGE;
     const int set = (kb / kKC) & 1, k = kb % kKC;
-    i32x8 bt[TT];
-    uint32_t sa[TT];
-#pragma unroll
-    for (int t = 0; t < TT; t++) {
-      const int r = wt * (BT / WT) + t * 16;
-      bt[t] = frag(st, r);
-      sa[t] = s_sa[set][k][r + fr];
-    }
+    i32x8 an[TN];
+    uint32_t sn[TN][HW ? 1 : 2];
 #pragma unroll
     for (int n = 0; n < TN; n++) {
       const int c = wn * (BN / WN) + n * 16;
-      const i32x8 an = frag(st, BT + c);
+      an[n] = frag(st, BT + c);
       const uint32_t *sw = s_sw[set][k][c / 16];
       if constexpr (HW) {
-        const uint32_t sn = sw[fr & 1];
-#pragma unroll
-        for (int t = 0; t < TT; t++)
-          acc[n][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(an, bt[t], acc[n][t], 0, 0, 0,
-                                                                       (int)sn, 0, (int)sa[t]);
+        sn[n][0] = sw[fr & 1];
       } else {
-        const float se = __uint_as_float(sw[0]), so = __uint_as_float(sw[1]);
+        sn[n][0] = sw[0];
+        sn[n][1] = sw[1];
+      }
+    }
+    // the next piece's operand is read while this one's products run
+    i32x8 bt = frag(st, wt * (BT / WT));
+    uint32_t sa = s_sa[set][k][wt * (BT / WT) + fr];
 #pragma unroll
-        for (int t = 0; t < TT; t++) {
+    for (int t = 0; t < TT; t++) {
+      const int r = wt * (BT / WT) + (t + 1 < TT ? t + 1 : t) * 16;
+      const i32x8 bt_n = frag(st, r);
+      const uint32_t sa_n = s_sa[set][k][r + fr];
+#pragma unroll
+      for (int n = 0; n < TN; n++) {
+        if constexpr (HW) {
+          acc[n][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(an[n], bt, acc[n][t], 0, 0, 0,
+                                                                       (int)sn[n][0], 0, (int)sa);
+        } else {
           const f32x4 z = {0, 0, 0, 0};
           const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              an, bt[t], z, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
-          const float x0 = __uint_as_float(sa[t]) * se, x1 = __uint_as_float(sa[t]) * so;
+              an[n], bt, z, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+          const float x0 = __uint_as_float(sa) * __uint_as_float(sn[n][0]);
+          const float x1 = __uint_as_float(sa) * __uint_as_float(sn[n][1]);
           acc[n][t][0] += d[0] * x0;
           acc[n][t][1] += d[1] * x1;
           acc[n][t][2] += d[2] * x0;
           acc[n][t][3] += d[3] * x1;
         }
       }
+      bt = bt_n;
+      sa = sa_n;
+      __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);   // LDS reads
+      __builtin_amdgcn_sched_group_barrier(0x008, TN, 0);  // matrix instructions
     }
   }
 
@@ -289,13 +335,21 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
         *(u32x4 *)(g.aq + (int64_t)(row0 + tok) * I + j) = *(const u32x4 *)(sq + tok * QLD + ch);
     }
   }
+  __syncthreads();  // the next tile's loads overwrite the stages
+  }  // tiles
 }
 
-constexpr int kBT = 128, kBN = 256;
+constexpr int kBT = 256, kBN = 256;
 
 template <bool HW, bool SWI>
-hipError_t go(const Fp8Args &g, int grid, hipStream_t st) {
-  hipLaunchKernelGGL((gemm_fp8_kernel<HW, SWI, kBT, kBN, 2, 4>), dim3(grid), dim3(512), 0, st, g);
+hipError_t go(const Fp8Args &g, int64_t grid, hipStream_t st) {
+  auto kern = gemm_fp8_kernel<HW, SWI, kBT, kBN, 2, 4>;
+  int dev = 0, ncu = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&ncu, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+    return hipErrorInvalidValue;
+  const int64_t most = (int64_t)(ncu + kNumXcd - 1) / kNumXcd * kNumXcd;
+  hipLaunchKernelGGL(kern, dim3((uint32_t)(grid < most ? grid : most)), dim3(512), 0, st, g);
   return hipGetLastError();
 }
 
@@ -314,8 +368,8 @@ hipError_t launch_gemm_fp8(bool swiglu, const Fp8Args &g, hipStream_t st) {
   if (grid < 0) return hipErrorInvalidValue;
   if (grid == 0) return hipSuccess;
   const bool hw = g.a_e8m0 && g.w_e8m0;
-  if (swiglu) return hw ? go<true, true>(g, (int)grid, st) : go<false, true>(g, (int)grid, st);
-  return hw ? go<true, false>(g, (int)grid, st) : go<false, false>(g, (int)grid, st);
+  if (swiglu) return hw ? go<true, true>(g, grid, st) : go<false, true>(g, grid, st);
+  return hw ? go<true, false>(g, grid, st) : go<false, false>(g, grid, st);
 }
 
 }  // namespace moe
