@@ -129,6 +129,7 @@ moe_status moe_grouped_gemm_fp8(const moe_metadata *meta, const void *a, const v
   Fp8Args g = fp8_args(meta, K, C);
   g.a = (const uint8_t *)a;
   g.a_rows = gather ? meta->x_gather_idx : nullptr;
+  g.a_span = gather ? meta->N : meta->capacity;
   g.a_scale = a_scale;
   g.a_e8m0 = a_scale_type == MOE_SCALE_E8M0;
   g.w = (const uint8_t *)w;
@@ -169,6 +170,7 @@ moe_status moe_expert_forward_fp8(const moe_metadata *meta, const void *x, const
   Fp8Args up = fp8_args(meta, H, 2 * I);
   up.a = (const uint8_t *)x;
   up.a_rows = meta->x_gather_idx;
+  up.a_span = meta->N;
   up.a_scale = x_scale;
   up.a_e8m0 = x_scale_type == MOE_SCALE_E8M0;
   up.w = (const uint8_t *)w_up;
@@ -180,6 +182,7 @@ moe_status moe_expert_forward_fp8(const moe_metadata *meta, const void *x, const
   up.concat = layout == MOE_GATEUP_CONCAT;
   Fp8Args dn = fp8_args(meta, I, H);
   dn.a = up.aq;
+  dn.a_span = meta->capacity;
   dn.a_scale = up.aq_scale;
   dn.a_e8m0 = 1;
   dn.w = (const uint8_t *)w_down;

@@ -43,6 +43,13 @@ __device__ __forceinline__ void load_to_lds(const void *p, uint32_t lds) {
                : "s"(lds), "v"(p)
                : "memory");
 }
+// the same from a uniform address plus a lane's 32-bit offset
+__device__ __forceinline__ void load_to_lds(const void *base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(lds), "v"(off), "s"(base)
+               : "memory");
+}
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
   return (uint32_t)__builtin_amdgcn_readfirstlane(
@@ -55,21 +62,24 @@ __device__ __forceinline__ float scale_value(const void *p, int e8m0, int64_t i)
 
 constexpr int kKC = 8;  // blocks of K whose scales LDS holds at a time (two such sets)
 
-// WT x WN waves; HW: both scales are e8m0
-template <bool HW, bool SWI, int BT, int BN, int WT, int WN>
-__global__ __launch_bounds__(64 * WT * WN, WT *WN == 8 ? 2 : 1) void gemm_fp8_kernel(Fp8Args g) {
+// WT x WN waves. HW: both scales are e8m0. FAR: rows are found by 64-bit addresses per lane and
+// chunks past K come from a page of zeros; else (K in whole blocks, each operand's bytes
+// counted in 32 bits) by a uniform address that moves along K and a fixed offset per lane.
+template <bool HW, bool SWI, bool FAR, int BT, int BN, int WT, int WN>
+__global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   constexpr int NT = 64 * WT * WN, NW = WT * WN;
   constexpr int TT = BT / WT / 16, TN = BN / WN / 16;  // 16 x 16 pieces of a wave
   constexpr int ROWS = BT + BN, STAGE = ROWS * kQB;
-  constexpr int LD = ROWS / 8 / NW;  // 1 KB loads per wave and stage
-  static_assert(ROWS % (8 * NW) == 0 && BT % (8 * NW) == 0, "a load is of one operand");
+  constexpr int LA = BT / 8 / NW, LB = BN / 8 / NW;  // 1 KB loads per wave and block
+  static_assert(BT % (8 * NW) == 0 && BN % (8 * NW) == 0, "a load is of one operand");
+  static_assert(LA + LB <= (TT - 1) * TN, "loads between the products");
   static_assert(!SWI || BN == 256, "a SwiGLU tile holds one block of 128 pairs");
-  constexpr int F = BN / 16;                     // column pieces of the tile
+  constexpr int F = BN / 16;  // column pieces of the tile
   constexpr int SA = kKC * BT / NT, SW = (kKC * F * 2 + NT - 1) / NT;  // scales per thread
   static_assert(kKC * BT % NT == 0 && NT % BT == 0, "whole rounds");
   __shared__ __attribute__((aligned(128))) uint8_t smem[2 * STAGE];
-  __shared__ uint32_t s_sa[2][kKC][BT];          // token scales (bits: e8m0 byte or fp32)
-  __shared__ uint32_t s_sw[2][kKC][F][2];        // weight scales of a piece's even and odd rows
+  __shared__ uint32_t s_sa[2][kKC][BT];    // token scales (bits: e8m0 byte or fp32)
+  __shared__ uint32_t s_sw[2][kKC][F][2];  // weight scales of a piece's even and odd rows
   __shared__ int s_tab[2 * (MOE_MAX_EXPERTS + 1)];
   int *s_pref = s_tab, *s_off = s_tab + MOE_MAX_EXPERTS + 1;
 
@@ -94,142 +104,221 @@ __global__ __launch_bounds__(64 * WT * WN, WT *WN == 8 ? 2 : 1) void gemm_fp8_ke
   const int64_t gq = G / kNumXcd;
   const int gr = (int)(G % kNumXcd);
   const int64_t tend = (x + 1) * gq + min(x + 1, gr);
+  const int stride = gridDim.x / kNumXcd;
   int64_t L = x * gq + min(x, gr) + blockIdx.x / kNumXcd;
+  if (L >= tend) return;
   const int nk = g.nbk, I = g.C >> 1;
   const uint32_t lds0 = lds_address(smem);
 
-  // ---- a tile: its expert, first row, rows and column tile; the rows of a stage that this
-  // lane loads, (wave + NW i) * 8 + lane / 8, and its chunk there; the scales it fetches
-  int e, nt, row0, rows;
-  const uint8_t *ptr[LD];
-  const int cs = (lane & 7) ^ ((lane >> 4) | ((wave & 1) << 2));  // chunk of every row of this lane
-  const int ck = cs * 16;
-  int64_t sa_row = 0;
-  auto w_row = [&](int n) {  // memory row of tile column n: SwiGLU tiles hold (gate, up) pairs
-    int c = nt * BN + n;
-    c = c < g.C ? c : g.C - 1;
-    return SWI && g.concat ? (c & 1 ? I : 0) + (c >> 1) : c;
+  // ---- a tile: its expert, first row, rows and column tile
+  struct Tile {
+    int e, nt, row0, rows;
   };
-  auto set_tile = [&](int64_t l_) {
+  auto find_tile = [&](int64_t l_) {
     // within an expert, groups of four row tiles, column tiles outer: the tiles that an XCD
     // works on at a time then share their rows as well as their weights
-    int lo = 0, hi = g.E - 1;  // largest e with s_pref[e] * ntn <= l_
+    int lo = 0, hi = g.E - 1;  // largest e with s_pref[e] <= mtile
     const int mtile = (int)(l_ / ntn);
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (s_pref[mid] <= mtile) lo = mid; else hi = mid - 1;
     }
-    e = __builtin_amdgcn_readfirstlane(lo);
     const int mte = s_pref[lo + 1] - s_pref[lo];
     const int l = (int)(l_ - (int64_t)s_pref[lo] * ntn);
     constexpr int GM = 4;
     const int gi = l / (GM * ntn), rem = l - gi * GM * ntn, gm = min(GM, mte - gi * GM);
-    nt = __builtin_amdgcn_readfirstlane(rem / gm);
-    const int mt = gi * GM + rem - rem / gm * gm;
-    row0 = __builtin_amdgcn_readfirstlane(s_off[lo] + mt * BT);
-    rows = __builtin_amdgcn_readfirstlane(min(BT, s_off[lo + 1] - row0));
-#pragma unroll
-    for (int i = 0; i < LD; i++) {
-      const int r = (wave + NW * i) * 8 + (lane >> 3);
-      if (NW * i * 8 < BT) {
-        const int s = row0 + (r < rows ? r : 0);
-        const int64_t m = g.a_rows ? g.a_rows[s] : s;
-        ptr[i] = g.a + m * g.K + ck;
-      } else {
-        ptr[i] = g.w + ((int64_t)e * g.C + w_row(r - BT)) * g.K + ck;
-      }
-    }
-    const int r = tid % BT, s = row0 + (r < rows ? r : 0);
-    sa_row = (g.a_rows ? (int64_t)g.a_rows[s] : s) * g.nbk;
+    const int nt = rem / gm, mt = gi * GM + rem - nt * gm;
+    const int row0 = s_off[lo] + mt * BT;
+    Tile t;
+    t.e = __builtin_amdgcn_readfirstlane(lo);
+    t.nt = __builtin_amdgcn_readfirstlane(nt);
+    t.row0 = __builtin_amdgcn_readfirstlane(row0);
+    t.rows = __builtin_amdgcn_readfirstlane(min(BT, s_off[lo + 1] - row0));
+    return t;
   };
-  auto issue = [&](int kb) {
-    const uint32_t st = lds0 + (kb & 1) * STAGE + wave * 1024;
-    const int k0 = kb * kQB;
-    const bool in = k0 + ck < g.K;
+  // An opaque copy: what is derived from it is computed where it is used and not kept in
+  // registers across the loops, where the sums need them.
+  auto here = [](uint32_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
+  };
+  // Rows of a stage that this lane loads: (wave + NW i) * 8 + lane / 8, all of them at the
+  // same chunk. Their memory rows (FAR) or offsets; last, the row whose scales this thread
+  // fetches.
+  const int ck = ((lane & 7) ^ ((lane >> 4) | ((wave & 1) << 2))) * 16;
+  uint32_t arow[LA], wrow[LB], srow;
+  uint32_t nrow[LA + 1];  // the next tile's token rows
+  auto token_rows = [&](const Tile &t) {
+    const int tid_ = (int)here(tid);
 #pragma unroll
-    for (int i = 0; i < LD; i++)
-      load_to_lds(in ? (const void *)(ptr[i] + k0) : (const void *)((const uint8_t *)g_zeros + ck),
-                  st + NW * i * 1024);
+    for (int i = 0; i <= LA; i++) {
+      const int r = i < LA ? (wave + NW * i) * 8 + ((tid_ & 63) >> 3) : tid_ % BT;
+      const int s = t.row0 + (r < t.rows ? r : 0);
+      nrow[i] = (uint32_t)(g.a_rows ? g.a_rows[s] : s);
+    }
+  };
+  // memory row of tile column n: SwiGLU tiles hold (gate, up) pairs
+  auto w_row = [&](const Tile &t, int n) {
+    int c = t.nt * BN + n;
+    c = c < g.C ? c : g.C - 1;
+    return SWI && g.concat ? (c & 1 ? I : 0) + (c >> 1) : c;
+  };
+  const uint8_t *pa, *pw;  // block to be loaded, of both operands
+  int kl;                  // its number
+  auto load_tile = [&](const Tile &t) {  // the loads' rows, from nrow
+    const int lane_ = (int)here(lane), c_ = (int)here(ck);
+#pragma unroll
+    for (int i = 0; i < LA; i++) arow[i] = FAR ? nrow[i] : nrow[i] * (uint32_t)g.K + c_;
+#pragma unroll
+    for (int i = 0; i < LB; i++) {
+      const uint32_t r = (uint32_t)w_row(t, (wave + NW * i) * 8 + (lane_ >> 3));
+      wrow[i] = FAR ? r : r * (uint32_t)g.K + c_;
+    }
+    pa = g.a;
+    pw = g.w + (int64_t)t.e * g.C * g.K;
+    kl = 0;
+  };
+  auto load = [&](uint32_t stage, int i) {
+    const uint32_t st = stage + wave * 1024 + NW * i * 1024;
+    if constexpr (!FAR) {
+      if (i < LA) load_to_lds(pa, arow[i], st);
+      else load_to_lds(pw, wrow[i - LA], st);
+    } else {
+      const uint32_t c = here(ck);
+      const uint8_t *p = (i < LA ? pa : pw) +
+                         ((uint64_t)here(i < LA ? arow[i] : wrow[i - LA]) * (uint32_t)g.K + c);
+      load_to_lds(kl * kQB + (int)c < g.K ? p : (const uint8_t *)g_zeros + c, st);
+    }
   };
   // ---- scales of kKC blocks from kb: fetched into registers, put into LDS later
   uint32_t ra[SA], rw[SW];
-  auto get_scales = [&](int kb) {
+  auto get_scales = [&](const Tile &t, uint32_t row, int kb) {
+    const int tid_ = (int)here(tid);
+    const int64_t base = (int64_t)here(row) * g.nbk;
 #pragma unroll
     for (int i = 0; i < SA; i++) {
-      const int64_t at = sa_row + min(kb + tid / BT + i * (NT / BT), nk - 1);
+      const int64_t at = base + min(kb + tid_ / BT + i * (NT / BT), nk - 1);
       ra[i] = HW ? (uint32_t)((const uint8_t *)g.a_scale)[at]
                  : __float_as_uint(scale_value(g.a_scale, g.a_e8m0, at));
     }
 #pragma unroll
     for (int i = 0; i < SW; i++) {
-      const int j = min(tid + NT * i, kKC * F * 2 - 1);
+      const int j = min(tid_ + NT * i, kKC * F * 2 - 1);
       const int k = j / (F * 2), f = (j >> 1) % F, odd = j & 1;
-      const int64_t at = ((int64_t)e * g.nbc + w_row(f * 16 + odd) / kQB) * g.nbk + min(kb + k, nk - 1);
+      const int64_t at =
+          ((int64_t)t.e * g.nbc + w_row(t, f * 16 + odd) / kQB) * g.nbk + min(kb + k, nk - 1);
       rw[i] = HW ? (uint32_t)((const uint8_t *)g.w_scale)[at]
                  : __float_as_uint(scale_value(g.w_scale, g.w_e8m0, at));
     }
   };
-  auto put_scales = [&](int kb) {
-    const int set = (kb / kKC) & 1;
+  auto put_scales = [&](int set) {
+    const int tid_ = (int)here(tid);
 #pragma unroll
-    for (int i = 0; i < SA; i++) s_sa[set][tid / BT + i * (NT / BT)][tid % BT] = ra[i];
+    for (int i = 0; i < SA; i++) s_sa[set][tid_ / BT + i * (NT / BT)][tid_ % BT] = ra[i];
 #pragma unroll
     for (int i = 0; i < SW; i++) {
-      const int j = tid + NT * i;
+      const int j = tid_ + NT * i;
       if (j < kKC * F * 2) (&s_sw[set][0][0][0])[j] = rw[i];
     }
   };
 
-  // operand of 16 rows from row r0 of a stage: lane l takes 32 bytes of row r0 + l % 16
+  // ---- LDS reads of a step. The operand of 16 rows: lane l takes 32 bytes of row l % 16, the
+  // chunks l / 16 and l / 16 + 4 (both operands alike, so any choice gives the same sums; this
+  // one reads at 250 B/clk per CU, chunks 2 (l / 16) and the next at 127, measured). Addresses
+  // of this wave's first rows (tokens, weights; first and second chunk) in the stage to be
+  // read next, and of its scales; pieces are constant offsets away.
   const int fr = lane & 15, fg = lane >> 4;
-  const int fsw = (fr >> 1) & 7;
-  const int fo0 = fr * kQB + (((2 * fg) ^ fsw) << 4), fo1 = fr * kQB + (((2 * fg + 1) ^ fsw) << 4);
-  auto frag = [&](const uint8_t *st, int r0) {
-    const i32x4 a = *(const i32x4 *)(st + r0 * kQB + fo0);
-    const i32x4 b = *(const i32x4 *)(st + r0 * kQB + fo1);
+  const uint32_t fo0 = lds0 + fr * kQB + ((fg ^ (fr >> 1)) << 4);
+  uint32_t ta0 = fo0 + wt * (BT / WT) * kQB, wa0 = fo0 + (BT + wn * (BN / WN)) * kQB;
+  uint32_t ta1 = ta0 ^ 64, wa1 = wa0 ^ 64;
+  const uint32_t la = lds_address(s_sa) + (wt * (BT / WT) + fr) * 4;
+  const uint32_t lw = lds_address(s_sw) + wn * (TN * 8) + (HW ? (fr & 1) * 4 : 0);
+  auto pair = [&](uint32_t a0, uint32_t a1, int off) {
+    typedef const __attribute__((address_space(3))) i32x4 *P;
+    const i32x4 a = *(P)(uintptr_t)(a0 + off), b = *(P)(uintptr_t)(a1 + off);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   };
+  auto word = [&](uint32_t a) {
+    return *(const __attribute__((address_space(3))) uint32_t *)(uintptr_t)a;
+  };
+  i32x8 an[TN], bt;
+  uint32_t sn[TN][HW ? 1 : 2], sa;
+  auto weights_piece = [&](int si, int n) {  // si: the block's place among the scales in LDS
+    an[n] = pair(wa0, wa1, n * 16 * kQB);
+    const uint32_t p = lw + si * (F * 8) + n * 8;
+    sn[n][0] = word(p);
+    if constexpr (!HW) sn[n][1] = word(p + 4);
+  };
+  auto tokens_piece = [&](int si, int t, i32x8 &v, uint32_t &s) {
+    v = pair(ta0, ta1, t * 16 * kQB);
+    s = word(la + si * (BT * 4) + t * 64);
+  };
 
-  for (; L < tend; L += gridDim.x / kNumXcd) {
-  set_tile(L);
+  // One step of the reduction multiplies the operands of one block. The weights' pieces are in
+  // registers when it begins, and the tokens' pieces are each read one piece ahead. Before the
+  // last piece every wave has read all of the stage, and its loads into the other one, made
+  // between the first pieces' products, are awaited: one barrier hands both over, and the next
+  // block's first operands are read while the last piece's products run. The block after a
+  // tile's last is the next tile's first, so its loads run under that step and the epilogue.
+  Tile tile = find_tile(L);
+  token_rows(tile);
+  load_tile(tile);
+  srow = nrow[LA];
+#pragma unroll
+  for (int i = 0; i < LA + LB; i++) load(lds0, i);
+  get_scales(tile, srow, 0);
+  put_scales(0);
+  wait_loads();
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < TN; n++) weights_piece(0, n);
+  tokens_piece(0, 0, bt, sa);
+  uint32_t stage = lds0;  // of the block being multiplied
+  int set = 0;            // its scales' set
+  for (;;) {
+  const bool more = L + stride < tend;
+  const Tile next = find_tile(more ? L + stride : L);  // the last tile: itself again, unused
+  token_rows(next);
   f32x4 acc[TN][TT];
 #pragma unroll
   for (int n = 0; n < TN; n++)
 #pragma unroll
     for (int t = 0; t < TT; t++) acc[n][t] = f32x4{0, 0, 0, 0};
-  issue(0);
-  get_scales(0);
-  put_scales(0);
   for (int kb = 0; kb < nk; kb++) {
-    wait_loads();
-    if (kb % kKC == kKC - 1 && kb + 1 < nk) put_scales(kb + 1);
-    __syncthreads();  // stage kb is there, and everyone is done with stage kb - 1
-    if (kb + 1 < nk) issue(kb + 1);
-    if (kb % kKC == 0 && kb + kKC < nk) get_scales(kb + kKC);
-    const uint8_t *st = smem + (kb & 1) * STAGE;
-    const int set = (kb / kKC) & 1, k = kb % kKC;
-    i32x8 an[TN];
-    uint32_t sn[TN][HW ? 1 : 2];
-#pragma unroll
-    for (int n = 0; n < TN; n++) {
-      const int c = wn * (BN / WN) + n * 16;
-      an[n] = frag(st, BT + c);
-      const uint32_t *sw = s_sw[set][k][c / 16];
-      if constexpr (HW) {
-        sn[n][0] = sw[fr & 1];
-      } else {
-        sn[n][0] = sw[0];
-        sn[n][1] = sw[1];
-      }
+    const int k = kb % kKC, len = min(kKC, nk - (kb - k));
+    const bool last = k == len - 1;  // of the blocks whose scales are in this set
+    if (k == len / 2) {
+      if (kb - k + kKC < nk) get_scales(tile, srow, kb - k + kKC);
+      else get_scales(next, nrow[LA], 0);
     }
-    // the next piece's operand is read while this one's products run
-    i32x8 bt = frag(st, wt * (BT / WT));
-    uint32_t sa = s_sa[set][k][wt * (BT / WT) + fr];
+    if (kb + 1 < nk) {
+      kl++;
+      pa += kQB;
+      pw += kQB;
+    } else {
+      load_tile(next);
+    }
+    const uint32_t other = stage ^ (lds0 ^ (lds0 + STAGE));
+    const int si = set * kKC + k;
 #pragma unroll
     for (int t = 0; t < TT; t++) {
-      const int r = wt * (BT / WT) + (t + 1 < TT ? t + 1 : t) * 16;
-      const i32x8 bt_n = frag(st, r);
-      const uint32_t sa_n = s_sa[set][k][r + fr];
+      int sj = si;
+      if (t + 1 == TT) {
+        wait_loads();
+        if (last) put_scales(set ^ 1);
+        __syncthreads();
+        const uint32_t d = other - stage;
+        ta0 += d;
+        ta1 += d;
+        wa0 += d;
+        wa1 += d;
+        stage = other;
+        sj = last ? (set ^ 1) * kKC : si + 1;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      i32x8 bt_n;
+      uint32_t sa_n;
+      tokens_piece(sj, t + 1 < TT ? t + 1 : 0, bt_n, sa_n);
 #pragma unroll
       for (int n = 0; n < TN; n++) {
         if constexpr (HW) {
@@ -246,21 +335,22 @@ __global__ __launch_bounds__(64 * WT * WN, WT *WN == 8 ? 2 : 1) void gemm_fp8_ke
           acc[n][t][2] += d[2] * x0;
           acc[n][t][3] += d[3] * x1;
         }
+        if (t + 1 == TT) weights_piece(sj, n);
+        if (t * TN + n < LA + LB) load(other, t * TN + n);
       }
       bt = bt_n;
       sa = sa_n;
-      __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);   // LDS reads
-      __builtin_amdgcn_sched_group_barrier(0x008, TN, 0);  // matrix instructions
+      // the pieces stay in this order: the compiler would gather the products behind the
+      // barrier, and hold all their operands until then
+#pragma unroll
+      for (int n = 0; n < TN; n++) asm volatile("" : "+v"(acc[n][t]));
+      __builtin_amdgcn_sched_barrier(0);
     }
+    if (last) set ^= 1;
   }
+  srow = nrow[LA];
 
-  // The sums are pinned here: a matrix instruction moved under a later per-lane condition
-  // would take its operands from loads that only the condition's lanes make.
-#pragma unroll
-  for (int n = 0; n < TN; n++)
-#pragma unroll
-    for (int t = 0; t < TT; t++) asm volatile("" : "+v"(acc[n][t]));
-
+  const int nt = tile.nt, row0 = tile.row0, rows = tile.rows;
   // ---- epilogues: acc[n][t] of lane l holds columns cb .. cb + 3 of token tok
   if constexpr (!SWI) {
 #pragma unroll
@@ -280,11 +370,12 @@ __global__ __launch_bounds__(64 * WT * WN, WT *WN == 8 ? 2 : 1) void gemm_fp8_ke
     // a = silu(gate) up; the block of 128 is the whole tile, so a token's maximum is taken
     // over the four lanes that share it and over the WN waves
     float av[TN][TT][2];
-    __syncthreads();  // everyone is done with the stages
-    uint32_t *red = (uint32_t *)smem;  // [WN][BT]
-    uint8_t *sq = smem + WN * BT * 4;  // [BT][128 + 16]
+    // in the stage that was just multiplied: everyone has read it
+    uint8_t *free_stage = smem + (stage == lds0 ? STAGE : 0);
+    uint32_t *red = (uint32_t *)free_stage;  // [WN][BT]
+    uint8_t *sq = free_stage + WN * BT * 4;  // [BT][128 + 16]
     constexpr int QLD = kQB + 16;
-    static_assert(WN * BT * 4 + BT * QLD <= 2 * STAGE, "epilogue fits the stages");
+    static_assert(WN * BT * 4 + BT * QLD <= STAGE, "epilogue fits a stage");
 #pragma unroll
     for (int t = 0; t < TT; t++) {
       const int tok = wt * (BT / WT) + t * 16 + fr;
@@ -335,15 +426,18 @@ __global__ __launch_bounds__(64 * WT * WN, WT *WN == 8 ? 2 : 1) void gemm_fp8_ke
         *(u32x4 *)(g.aq + (int64_t)(row0 + tok) * I + j) = *(const u32x4 *)(sq + tok * QLD + ch);
     }
   }
-  __syncthreads();  // the next tile's loads overwrite the stages
+  if (!more) break;
+  if constexpr (SWI) __syncthreads();  // the next step loads over the epilogue's LDS
+  L += stride;
+  tile = next;
   }  // tiles
 }
 
 constexpr int kBT = 256, kBN = 256;
 
-template <bool HW, bool SWI>
+template <bool HW, bool SWI, bool FAR>
 hipError_t go(const Fp8Args &g, int64_t grid, hipStream_t st) {
-  auto kern = gemm_fp8_kernel<HW, SWI, kBT, kBN, 2, 4>;
+  auto kern = gemm_fp8_kernel<HW, SWI, FAR, kBT, kBN, 2, 4>;
   int dev = 0, ncu = 0;
   if (hipGetDevice(&dev) != hipSuccess ||
       hipDeviceGetAttribute(&ncu, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
@@ -351,6 +445,12 @@ hipError_t go(const Fp8Args &g, int64_t grid, hipStream_t st) {
   const int64_t most = (int64_t)(ncu + kNumXcd - 1) / kNumXcd * kNumXcd;
   hipLaunchKernelGGL(kern, dim3((uint32_t)(grid < most ? grid : most)), dim3(512), 0, st, g);
   return hipGetLastError();
+}
+template <bool HW, bool SWI>
+hipError_t go(const Fp8Args &g, int64_t grid, hipStream_t st) {
+  const bool near = g.K % kQB == 0 && (int64_t)g.a_span * g.K <= 0xffffffffll &&
+                    (int64_t)g.C * g.K <= 0xffffffffll;
+  return near ? go<HW, SWI, false>(g, grid, st) : go<HW, SWI, true>(g, grid, st);
 }
 
 }  // namespace

@@ -187,6 +187,7 @@ struct Fp8Args {
   int C, K;  // output columns and reduction length
   const uint8_t *a;
   const int32_t *a_rows;  // row map (gather) or null = identity
+  int a_span;             // rows of a
   const void *a_scale;
   const uint8_t *w;
   const void *w_scale;
