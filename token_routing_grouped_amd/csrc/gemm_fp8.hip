@@ -72,7 +72,6 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   constexpr int ROWS = BT + BN, STAGE = ROWS * kQB;
   constexpr int LA = BT / 8 / NW, LB = BN / 8 / NW;  // 1 KB loads per wave and block
   static_assert(BT % (8 * NW) == 0 && BN % (8 * NW) == 0, "a load is of one operand");
-  static_assert(LA + LB <= (TT - 1) * TN, "loads between the products");
   static_assert(!SWI || BN == 256, "a SwiGLU tile holds one block of 128 pairs");
   constexpr int F = BN / 16;  // column pieces of the tile
   constexpr int SA = kKC * BT / NT, SW = (kKC * F * 2 + NT - 1) / NT;  // scales per thread
@@ -80,6 +79,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   __shared__ __attribute__((aligned(128))) uint8_t smem[2 * STAGE];
   __shared__ uint32_t s_sa[2][kKC][BT];    // token scales (bits: e8m0 byte or fp32)
   __shared__ uint32_t s_sw[2][kKC][F][2];  // weight scales of a piece's even and odd rows
+  __shared__ uint32_t s_max[SWI ? WN : 1][SWI ? BT : 1];  // a token's largest |a|, per wave
   __shared__ int s_tab[2 * (MOE_MAX_EXPERTS + 1)];
   int *s_pref = s_tab, *s_off = s_tab + MOE_MAX_EXPERTS + 1;
 
@@ -107,22 +107,20 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   const int stride = gridDim.x / kNumXcd;
   int64_t L = x * gq + min(x, gr) + blockIdx.x / kNumXcd;
   if (L >= tend) return;
-  const int nk = g.nbk, I = g.C >> 1;
+  // two blocks at least: a tile is entered by its first two (FAR: what is past K is zeros)
+  const int nk = FAR ? max(g.nbk, 2) : g.nbk, I = g.C >> 1;
   const uint32_t lds0 = lds_address(smem);
 
   // ---- a tile: its expert, first row, rows and column tile
   struct Tile {
     int e, nt, row0, rows;
   };
-  auto find_tile = [&](int64_t l_) {
+  auto find_tile = [&](int64_t l_, int lo) {
     // within an expert, groups of four row tiles, column tiles outer: the tiles that an XCD
-    // works on at a time then share their rows as well as their weights
-    int lo = 0, hi = g.E - 1;  // largest e with s_pref[e] <= mtile
+    // works on at a time then share their rows as well as their weights. The expert is the
+    // last e with s_pref[e] <= mtile, from lo on: a workgroup's tiles ascend.
     const int mtile = (int)(l_ / ntn);
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_pref[mid] <= mtile) lo = mid; else hi = mid - 1;
-    }
+    while (s_pref[lo + 1] <= mtile) lo++;
     const int mte = s_pref[lo + 1] - s_pref[lo];
     const int l = (int)(l_ - (int64_t)s_pref[lo] * ntn);
     constexpr int GM = 4;
@@ -178,6 +176,11 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
     pw = g.w + (int64_t)t.e * g.C * g.K;
     kl = 0;
   };
+  auto advance = [&] {
+    kl++;
+    pa += kQB;
+    pw += kQB;
+  };
   auto load = [&](uint32_t stage, int i) {
     const uint32_t st = stage + wave * 1024 + NW * i * 1024;
     if constexpr (!FAR) {
@@ -197,7 +200,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
     const int64_t base = (int64_t)here(row) * g.nbk;
 #pragma unroll
     for (int i = 0; i < SA; i++) {
-      const int64_t at = base + min(kb + tid_ / BT + i * (NT / BT), nk - 1);
+      const int64_t at = base + min(kb + tid_ / BT + i * (NT / BT), g.nbk - 1);
       ra[i] = HW ? (uint32_t)((const uint8_t *)g.a_scale)[at]
                  : __float_as_uint(scale_value(g.a_scale, g.a_e8m0, at));
     }
@@ -206,7 +209,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
       const int j = min(tid_ + NT * i, kKC * F * 2 - 1);
       const int k = j / (F * 2), f = (j >> 1) % F, odd = j & 1;
       const int64_t at =
-          ((int64_t)t.e * g.nbc + w_row(t, f * 16 + odd) / kQB) * g.nbk + min(kb + k, nk - 1);
+          ((int64_t)t.e * g.nbc + w_row(t, f * 16 + odd) / kQB) * g.nbk + min(kb + k, g.nbk - 1);
       rw[i] = HW ? (uint32_t)((const uint8_t *)g.w_scale)[at]
                  : __float_as_uint(scale_value(g.w_scale, g.w_e8m0, at));
     }
@@ -241,49 +244,77 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   auto word = [&](uint32_t a) {
     return *(const __attribute__((address_space(3))) uint32_t *)(uintptr_t)a;
   };
-  i32x8 an[TN], bt;
-  uint32_t sn[TN][HW ? 1 : 2], sa;
+  i32x8 an[TN], bt[3];  // tokens' pieces: t in bt[t % 3]
+  uint32_t sn[TN][HW ? 1 : 2], sa[3];
   auto weights_piece = [&](int si, int n) {  // si: the block's place among the scales in LDS
     an[n] = pair(wa0, wa1, n * 16 * kQB);
     const uint32_t p = lw + si * (F * 8) + n * 8;
     sn[n][0] = word(p);
     if constexpr (!HW) sn[n][1] = word(p + 4);
   };
-  auto tokens_piece = [&](int si, int t, i32x8 &v, uint32_t &s) {
-    v = pair(ta0, ta1, t * 16 * kQB);
-    s = word(la + si * (BT * 4) + t * 64);
+  auto tokens_piece = [&](int si, int t) {
+    bt[t % 3] = pair(ta0, ta1, t * 16 * kQB);
+    sa[t % 3] = word(la + si * (BT * 4) + t * 64);
+  };
+  auto tokens_next = [&](int si) {  // the next block's first piece
+    bt[TT % 3] = pair(ta0, ta1, 0);
+    sa[TT % 3] = word(la + si * (BT * 4));
   };
 
   // One step of the reduction multiplies the operands of one block. The weights' pieces are in
-  // registers when it begins, and the tokens' pieces are each read one piece ahead. Before the
-  // last piece every wave has read all of the stage, and its loads into the other one, made
-  // between the first pieces' products, are awaited: one barrier hands both over, and the next
-  // block's first operands are read while the last piece's products run. The block after a
-  // tile's last is the next tile's first, so its loads run under that step and the epilogue.
-  Tile tile = find_tile(L);
+  // registers when it begins, and the tokens' pieces are read ahead of their products. With
+  // two pieces left, their operands in registers, every wave has read all of the stage, and
+  // its loads into the other one, made a step ago, are awaited: one barrier hands both over.
+  // The last two pieces' products then cover the loads of the block after next into the free
+  // stage and the reads of the next block's weights, each piece as soon as its registers are
+  // free. A tile's last two steps load the next tile's first blocks, so these are under way
+  // during the epilogue.
+  Tile tile = find_tile(L, 0);
   token_rows(tile);
   load_tile(tile);
   srow = nrow[LA];
 #pragma unroll
   for (int i = 0; i < LA + LB; i++) load(lds0, i);
   get_scales(tile, srow, 0);
+  advance();
+#pragma unroll
+  for (int i = 0; i < LA + LB; i++) load(lds0 + STAGE, i);
   put_scales(0);
   wait_loads();
   __syncthreads();
 #pragma unroll
   for (int n = 0; n < TN; n++) weights_piece(0, n);
-  tokens_piece(0, 0, bt, sa);
+  tokens_piece(0, 0);
   uint32_t stage = lds0;  // of the block being multiplied
   int set = 0;            // its scales' set
   for (;;) {
   const bool more = L + stride < tend;
-  const Tile next = find_tile(more ? L + stride : L);  // the last tile: itself again, unused
+  const Tile next = find_tile(more ? L + stride : L, tile.e);  // the last tile: itself, unused
   token_rows(next);
   f32x4 acc[TN][TT];
 #pragma unroll
   for (int n = 0; n < TN; n++)
 #pragma unroll
     for (int t = 0; t < TT; t++) acc[n][t] = f32x4{0, 0, 0, 0};
+  auto multiply = [&](int n, int t) {
+    if constexpr (HW) {
+      acc[n][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+          an[n], bt[t % 3], acc[n][t], 0, 0, 0, (int)sn[n][0], 0, (int)sa[t % 3]);
+    } else {
+      const f32x4 z = {0, 0, 0, 0};
+      const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+          an[n], bt[t % 3], z, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+      const float x0 = __uint_as_float(sa[t % 3]) * __uint_as_float(sn[n][0]);
+      const float x1 = __uint_as_float(sa[t % 3]) * __uint_as_float(sn[n][1]);
+      acc[n][t][0] += d[0] * x0;
+      acc[n][t][1] += d[1] * x1;
+      acc[n][t][2] += d[2] * x0;
+      acc[n][t][3] += d[3] * x1;
+    }
+    // pinned to this place: the compiler would gather the products behind the barrier, and
+    // hold all their operands until then
+    asm volatile("" : "+v"(acc[n][t]));
+  };
   for (int kb = 0; kb < nk; kb++) {
     const int k = kb % kKC, len = min(kKC, nk - (kb - k));
     const bool last = k == len - 1;  // of the blocks whose scales are in this set
@@ -291,62 +322,43 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
       if (kb - k + kKC < nk) get_scales(tile, srow, kb - k + kKC);
       else get_scales(next, nrow[LA], 0);
     }
-    if (kb + 1 < nk) {
-      kl++;
-      pa += kQB;
-      pw += kQB;
-    } else {
-      load_tile(next);
-    }
-    const uint32_t other = stage ^ (lds0 ^ (lds0 + STAGE));
     const int si = set * kKC + k;
 #pragma unroll
-    for (int t = 0; t < TT; t++) {
-      int sj = si;
-      if (t + 1 == TT) {
-        wait_loads();
-        if (last) put_scales(set ^ 1);
-        __syncthreads();
-        const uint32_t d = other - stage;
-        ta0 += d;
-        ta1 += d;
-        wa0 += d;
-        wa1 += d;
-        stage = other;
-        sj = last ? (set ^ 1) * kKC : si + 1;
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      i32x8 bt_n;
-      uint32_t sa_n;
-      tokens_piece(sj, t + 1 < TT ? t + 1 : 0, bt_n, sa_n);
+    for (int t = 0; t < TT - 2; t++) {
+      if (t + 1 < TT - 2) tokens_piece(si, t + 1);
+      if (t + 1 == TT - 3) tokens_piece(si, TT - 2);
+      if (t == TT - 3) tokens_piece(si, TT - 1);
 #pragma unroll
-      for (int n = 0; n < TN; n++) {
-        if constexpr (HW) {
-          acc[n][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(an[n], bt, acc[n][t], 0, 0, 0,
-                                                                       (int)sn[n][0], 0, (int)sa);
-        } else {
-          const f32x4 z = {0, 0, 0, 0};
-          const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              an[n], bt, z, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
-          const float x0 = __uint_as_float(sa) * __uint_as_float(sn[n][0]);
-          const float x1 = __uint_as_float(sa) * __uint_as_float(sn[n][1]);
-          acc[n][t][0] += d[0] * x0;
-          acc[n][t][1] += d[1] * x1;
-          acc[n][t][2] += d[2] * x0;
-          acc[n][t][3] += d[3] * x1;
-        }
-        if (t + 1 == TT) weights_piece(sj, n);
-        if (t * TN + n < LA + LB) load(other, t * TN + n);
-      }
-      bt = bt_n;
-      sa = sa_n;
-      // the pieces stay in this order: the compiler would gather the products behind the
-      // barrier, and hold all their operands until then
-#pragma unroll
-      for (int n = 0; n < TN; n++) asm volatile("" : "+v"(acc[n][t]));
+      for (int n = 0; n < TN; n++) multiply(n, t);
       __builtin_amdgcn_sched_barrier(0);
     }
+    wait_loads();
+    if (last) put_scales(set ^ 1);
+    __syncthreads();
+    const uint32_t other = stage ^ (lds0 ^ (lds0 + STAGE)), d = other - stage;
+    ta0 += d;
+    ta1 += d;
+    wa0 += d;
+    wa1 += d;
+    if (kb + 2 == nk) load_tile(next);
+    else advance();
+    const int sj = last ? (set ^ 1) * kKC : si + 1;
+    static_assert((TT - 3) % 3 == TT % 3, "the piece after the last takes the free operand");
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < TN; n++) {
+      multiply(n, TT - 2);
+      multiply(n, TT - 1);
+      weights_piece(sj, n);
+      if (n == 0) tokens_next(sj);
+#pragma unroll
+      for (int i = n * (LA + LB) / TN; i < (n + 1) * (LA + LB) / TN; i++) load(stage, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    stage = other;
     if (last) set ^= 1;
+    bt[0] = bt[TT % 3];
+    sa[0] = sa[TT % 3];
   }
   srow = nrow[LA];
 
@@ -370,12 +382,6 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
     // a = silu(gate) up; the block of 128 is the whole tile, so a token's maximum is taken
     // over the four lanes that share it and over the WN waves
     float av[TN][TT][2];
-    // in the stage that was just multiplied: everyone has read it
-    uint8_t *free_stage = smem + (stage == lds0 ? STAGE : 0);
-    uint32_t *red = (uint32_t *)free_stage;  // [WN][BT]
-    uint8_t *sq = free_stage + WN * BT * 4;  // [BT][128 + 16]
-    constexpr int QLD = kQB + 16;
-    static_assert(WN * BT * 4 + BT * QLD <= STAGE, "epilogue fits a stage");
 #pragma unroll
     for (int t = 0; t < TT; t++) {
       const int tok = wt * (BT / WT) + t * 16 + fr;
@@ -400,34 +406,40 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
         const uint32_t u = (uint32_t)__shfl_xor((int)m, s, kWave);
         m = m > u ? m : u;
       }
-      if (fg == 0) red[wn * BT + tok] = m;
+      if (fg == 0) s_max[wn][tok] = m;
     }
     __syncthreads();
+    static_assert(TN == 4, "four pieces, one for each lane that shares a token");
 #pragma unroll
     for (int t = 0; t < TT; t++) {
       const int tok = wt * (BT / WT) + t * 16 + fr;
-      uint32_t m = red[tok];
+      uint32_t m = s_max[0][tok];
 #pragma unroll
-      for (int w = 1; w < WN; w++) m = m > red[w * BT + tok] ? m : red[w * BT + tok];
+      for (int w = 1; w < WN; w++) m = m > s_max[w][tok] ? m : s_max[w][tok];
       const uint32_t ex = scale_exponent(m);
       const float inv = exponent_inverse(ex);
-#pragma unroll
-      for (int n = 0; n < TN; n++) {
-        const uint32_t q = pack_e4m3(to_q(av[n][t][0], inv), to_q(av[n][t][1], inv), 0.0f, 0.0f);
-        *(uint16_t *)(sq + tok * QLD + (wn * (BN / WN) + n * 16 + fg * 4) / 2) = (uint16_t)q;
-      }
+      // The lane's two bytes of each piece; the four lanes of a token then exchange them, so
+      // that lane fg has the eight bytes of piece fg.
+      const uint32_t a01 = pack_e4m3(to_q(av[0][t][0], inv), to_q(av[0][t][1], inv),
+                                     to_q(av[1][t][0], inv), to_q(av[1][t][1], inv));
+      const uint32_t a23 = pack_e4m3(to_q(av[2][t][0], inv), to_q(av[2][t][1], inv),
+                                     to_q(av[3][t][0], inv), to_q(av[3][t][1], inv));
+      const bool up = fg & 2, odd = fg & 1;
+      const uint32_t mine = up ? a23 : a01;
+      const uint32_t his = (uint32_t)__shfl_xor((int)(up ? a01 : a23), 32, kWave);
+      const uint32_t w0 = up ? his : mine, w1 = up ? mine : his;  // of lanes fg & 1, 2 + fg & 1
+      const uint32_t keep = odd ? (w0 >> 16) | (w1 & 0xffff0000u) : (w0 & 0xffffu) | (w1 << 16);
+      const uint32_t give = odd ? (w0 & 0xffffu) | (w1 << 16) : (w0 >> 16) | (w1 & 0xffff0000u);
+      const uint32_t got = (uint32_t)__shfl_xor((int)give, 16, kWave);
+      const uint32_t ev = odd ? got : keep, od = odd ? keep : got;  // of even and odd lanes
+      const u32x2 q = {(ev & 0xffffu) | (od << 16), (ev >> 16) | (od & 0xffff0000u)};
+      const int j = nt * kQB + wn * (BN / WN / 2) + fg * 8;
+      if (tok < rows && j < I) *(u32x2 *)(g.aq + (int64_t)(row0 + tok) * I + j) = q;
       if (wn == 0 && fg == 0 && tok < rows)
         g.aq_scale[(int64_t)(row0 + tok) * ((I + kQB - 1) / kQB) + nt] = (uint8_t)ex;
     }
-    __syncthreads();
-    for (int i = tid; i < BT * 8; i += NT) {
-      const int tok = i >> 3, ch = (i & 7) * 16, j = nt * kQB + ch;
-      if (tok < rows && j < I)
-        *(u32x4 *)(g.aq + (int64_t)(row0 + tok) * I + j) = *(const u32x4 *)(sq + tok * QLD + ch);
-    }
   }
   if (!more) break;
-  if constexpr (SWI) __syncthreads();  // the next step loads over the epilogue's LDS
   L += stride;
   tile = next;
   }  // tiles
@@ -448,7 +460,7 @@ hipError_t go(const Fp8Args &g, int64_t grid, hipStream_t st) {
 }
 template <bool HW, bool SWI>
 hipError_t go(const Fp8Args &g, int64_t grid, hipStream_t st) {
-  const bool near = g.K % kQB == 0 && (int64_t)g.a_span * g.K <= 0xffffffffll &&
+  const bool near = g.K % kQB == 0 && g.nbk > 1 && (int64_t)g.a_span * g.K <= 0xffffffffll &&
                     (int64_t)g.C * g.K <= 0xffffffffll;
   return near ? go<HW, SWI, false>(g, grid, st) : go<HW, SWI, true>(g, grid, st);
 }
