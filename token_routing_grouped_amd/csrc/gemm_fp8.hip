@@ -62,6 +62,25 @@ __device__ __forceinline__ float scale_value(const void *p, int e8m0, int64_t i)
 
 constexpr int kKC = 8;  // blocks of K whose scales LDS holds at a time (two such sets)
 
+// Four lanes that share a token (16 apart) hold four consecutive bf16 columns each of pieces
+// n and n + 1: a[0..1] and b[0..1]. They exchange them, so that lane r of the four has the
+// eight columns 8 r .. 8 r + 7 of the 32 and a store takes 64 bytes of every row (stores as
+// the lanes hold them, 8 bytes each, cost 18 % of the largest product's time).
+__device__ __forceinline__ u32x4 columns8(u32x2 a, u32x2 b) {
+  u32x4 v;
+#pragma unroll
+  for (int j = 0; j < 2; j++) {
+    const auto h = __builtin_amdgcn_permlane32_swap(a[j], b[j], false, false);
+    const auto q = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
+    v[j] = q[0];
+    v[2 + j] = q[1];
+  }
+  return v;
+}
+__device__ __forceinline__ u32x2 to_bf16(const f32x4 &v) {
+  return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+
 // WT x WN waves. HW: both scales are e8m0. FAR: rows are found by 64-bit addresses per lane and
 // chunks past K come from a page of zeros; else (K in whole blocks, each operand's bytes
 // counted in 32 bits) by a uniform address that moves along K and a fixed offset per lane.
@@ -363,21 +382,22 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   srow = nrow[LA];
 
   const int nt = tile.nt, row0 = tile.row0, rows = tile.rows;
-  // ---- epilogues: acc[n][t] of lane l holds columns cb .. cb + 3 of token tok
+  // ---- epilogues: acc[n][t] of lane l holds columns 16 n + 4 (l / 16) .. + 3 of token
+  // 16 t + l % 16 of its wave
+  // bf16 rows of piece t, two column pieces at a time
+  auto store_rows = [&](int t) {
+    const int tok = wt * (BT / WT) + t * 16 + fr;
+    uint16_t *o = g.out + (int64_t)(row0 + tok) * g.C;
+#pragma unroll
+    for (int n = 0; n < TN; n += 2) {
+      const u32x4 v = columns8(to_bf16(acc[n][t]), to_bf16(acc[n + 1][t]));
+      const int c = nt * BN + wn * (BN / WN) + n * 16 + fg * 8;
+      if (tok < rows && c < g.C) *(u32x4 *)(o + c) = v;
+    }
+  };
   if constexpr (!SWI) {
 #pragma unroll
-    for (int t = 0; t < TT; t++) {
-      const int tok = wt * (BT / WT) + t * 16 + fr;
-      if (tok >= rows) continue;
-      const int64_t o = (int64_t)(row0 + tok) * g.C;
-#pragma unroll
-      for (int n = 0; n < TN; n++) {
-        const int c = nt * BN + wn * (BN / WN) + n * 16 + fg * 4;
-        if (c >= g.C) continue;
-        const f32x4 v = acc[n][t];
-        *(u32x2 *)(g.out + o + c) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-      }
-    }
+    for (int t = 0; t < TT; t++) store_rows(t);
   } else {
     // a = silu(gate) up; the block of 128 is the whole tile, so a token's maximum is taken
     // over the four lanes that share it and over the WN waves
@@ -385,15 +405,13 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
 #pragma unroll
     for (int t = 0; t < TT; t++) {
       const int tok = wt * (BT / WT) + t * 16 + fr;
-      const int64_t o = (int64_t)(row0 + tok) * g.C;
+      if (g.out) store_rows(t);
       uint32_t m = 0;
 #pragma unroll
       for (int n = 0; n < TN; n++) {
         const int c = nt * BN + wn * (BN / WN) + n * 16 + fg * 4;
         const bool in = c < g.C;
         const f32x4 v = acc[n][t];
-        if (g.out && in && tok < rows)
-          *(u32x2 *)(g.out + o + c) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 #pragma unroll
         for (int p = 0; p < 2; p++) {
           av[n][t][p] = in ? silu_f(v[2 * p]) * v[2 * p + 1] : 0.0f;
