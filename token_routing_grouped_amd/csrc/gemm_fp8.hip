@@ -51,6 +51,11 @@ __device__ __forceinline__ void load_to_lds(const void *base, uint32_t off, uint
                : "memory");
 }
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// all but the last N memory operations of this wave (they count down in order of issue)
+template <int N>
+__device__ __forceinline__ void wait_loads_before() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
   return (uint32_t)__builtin_amdgcn_readfirstlane(
       (int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p);
@@ -306,6 +311,11 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   tokens_piece(0, 0);
   uint32_t stage = lds0;  // of the block being multiplied
   int set = 0;            // its scales' set
+  // Tokens past the segment repeat its first row, operands and scales, so they may store its
+  // results again; where the columns fill whole tiles every store can then be issued.
+  const bool even = g.C % BN == 0;
+  constexpr int STORES = SWI ? TT : TT * TN / 2;
+  bool stored = false;
   for (;;) {
   const bool more = L + stride < tend;
   const Tile next = find_tile(more ? L + stride : L, tile.e);  // the last tile: itself, unused
@@ -351,7 +361,10 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
       for (int n = 0; n < TN; n++) multiply(n, t);
       __builtin_amdgcn_sched_barrier(0);
     }
-    wait_loads();
+    // after an epilogue whose stores are all issued: not for those, only for the loads ahead
+    // of them
+    if (stored && kb == 0) wait_loads_before<STORES>();
+    else wait_loads();
     if (last) put_scales(set ^ 1);
     __syncthreads();
     const uint32_t other = stage ^ (lds0 ^ (lds0 + STAGE)), d = other - stage;
@@ -387,12 +400,12 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   // bf16 rows of piece t, two column pieces at a time
   auto store_rows = [&](int t) {
     const int tok = wt * (BT / WT) + t * 16 + fr;
-    uint16_t *o = g.out + (int64_t)(row0 + tok) * g.C;
+    uint16_t *o = g.out + (int64_t)(row0 + (tok < rows ? tok : 0)) * g.C;
 #pragma unroll
     for (int n = 0; n < TN; n += 2) {
       const u32x4 v = columns8(to_bf16(acc[n][t]), to_bf16(acc[n + 1][t]));
       const int c = nt * BN + wn * (BN / WN) + n * 16 + fg * 8;
-      if (tok < rows && c < g.C) *(u32x4 *)(o + c) = v;
+      if (even || (tok < rows && c < g.C)) *(u32x4 *)(o + c) = v;
     }
   };
   if constexpr (!SWI) {
@@ -414,9 +427,10 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
         const f32x4 v = acc[n][t];
 #pragma unroll
         for (int p = 0; p < 2; p++) {
-          av[n][t][p] = in ? silu_f(v[2 * p]) * v[2 * p + 1] : 0.0f;
-          const uint32_t b = finite_abs_bits(av[n][t][p]);
-          m = m > b ? m : b;
+          const float a = silu_fast(v[2 * p]) * v[2 * p + 1];  // a few 2^-24, far below h's error
+          const uint32_t b = finite_abs_bits(a);
+          av[n][t][p] = a;
+          m = in && b > m ? b : m;
         }
       }
 #pragma unroll
@@ -452,13 +466,15 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
       const uint32_t ev = odd ? got : keep, od = odd ? keep : got;  // of even and odd lanes
       const u32x2 q = {(ev & 0xffffu) | (od << 16), (ev >> 16) | (od & 0xffff0000u)};
       const int j = nt * kQB + wn * (BN / WN / 2) + fg * 8;
-      if (tok < rows && j < I) *(u32x2 *)(g.aq + (int64_t)(row0 + tok) * I + j) = q;
+      if (even || (tok < rows && j < I))
+        *(u32x2 *)(g.aq + (int64_t)(row0 + (tok < rows ? tok : 0)) * I + j) = q;
       if (wn == 0 && fg == 0 && tok < rows)
         g.aq_scale[(int64_t)(row0 + tok) * ((I + kQB - 1) / kQB) + nt] = (uint8_t)ex;
     }
   }
   if (!more) break;
   L += stride;
+  stored = even;
   tile = next;
   }  // tiles
 }
