@@ -479,11 +479,9 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   }  // tiles
 }
 
-constexpr int kBT = 256, kBN = 256;
-
 template <bool HW, bool SWI, bool FAR>
 hipError_t go(const Fp8Args &g, int64_t grid, hipStream_t st) {
-  auto kern = gemm_fp8_kernel<HW, SWI, FAR, kBT, kBN, 2, 4>;
+  auto kern = gemm_fp8_kernel<HW, SWI, FAR, 256, 256, 2, 4>;
   int dev = 0, ncu = 0;
   if (hipGetDevice(&dev) != hipSuccess ||
       hipDeviceGetAttribute(&ncu, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
@@ -501,18 +499,13 @@ hipError_t go(const Fp8Args &g, int64_t grid, hipStream_t st) {
 
 }  // namespace
 
-// Workgroups: row tiles of every segment, bounded from the capacity, times column tiles, in
-// whole rounds of the XCDs; fewer than 2^32 lanes in a launch.
-int64_t fp8_grid(bool swiglu, const Fp8Args &g) {
-  const int64_t mt = ((int64_t)g.cap + (int64_t)g.E * (kBT - 1)) / kBT;
-  const int64_t grid = (mt * ((g.C + kBN - 1) / kBN) + kNumXcd - 1) / kNumXcd * kNumXcd;
-  return grid > (1 << 23) - kNumXcd ? -1 : grid;
-}
-
 hipError_t launch_gemm_fp8(bool swiglu, const Fp8Args &g, hipStream_t st) {
   const int64_t grid = fp8_grid(swiglu, g);
   if (grid < 0) return hipErrorInvalidValue;
   if (grid == 0) return hipSuccess;
+  int bt, bn;
+  fp8_tile(swiglu, g, &bt, &bn);
+  if (bt <= 64) return launch_gemm_fp8_skinny(swiglu, g, bt, grid, st);
   const bool hw = g.a_e8m0 && g.w_e8m0;
   if (swiglu) return hw ? go<true, true>(g, grid, st) : go<false, true>(g, grid, st);
   return hw ? go<true, false>(g, grid, st) : go<false, false>(g, grid, st);

@@ -199,7 +199,11 @@ struct Fp8Args {
   uint8_t *aq_scale;
   int concat;  // rows of w (and its scale blocks) are [gates | ups]
 };
-int64_t fp8_grid(bool swiglu, const Fp8Args &g);  // -1: too large
+// rows and columns of a tile, and the workgroups of a launch (-1: too many)
+void fp8_tile(bool swiglu, const Fp8Args &g, int *bt, int *bn);
+int64_t fp8_grid(bool swiglu, const Fp8Args &g);
+hipError_t launch_gemm_fp8_skinny(bool swiglu, const Fp8Args &g, int bt, int64_t grid,
+                                  hipStream_t st);
 hipError_t launch_gemm_fp8(bool swiglu, const Fp8Args &g, hipStream_t st);
 
 }  // namespace moe

@@ -84,4 +84,23 @@ int gemm_grid_f32(GemmKind kind, const GemmArgs &g) {
   return grid > 0x7fffffff ? -1 : (int)grid;
 }
 
+// 8-bit products. Few rows per expert on average (from the capacity): 16, 32 or 64-row tiles
+// of the weight-streaming kernel, 128 columns wide (SwiGLU: 256, one block of 128 pairs).
+void fp8_tile(bool swiglu, const Fp8Args &g, int *bt, int *bn) {
+  const int64_t cap = g.cap, E = g.E;
+  *bt = cap <= 8 * E ? 16 : cap <= 24 * E ? 32 : cap <= 64 * E ? 64 : 256;
+  *bn = *bt > 64 || swiglu ? 256 : 128;
+}
+
+// Row tiles of every segment, bounded from the capacity, times column tiles, in whole rounds
+// of the XCDs; fewer than 2^32 lanes in a launch.
+int64_t fp8_grid(bool swiglu, const Fp8Args &g) {
+  int bt, bn;
+  fp8_tile(swiglu, g, &bt, &bn);
+  int64_t mt = ((int64_t)g.cap + (int64_t)g.E * (bt - 1)) / bt;
+  if (mt > g.cap) mt = g.cap;  // no segment of a tile is empty
+  const int64_t grid = (mt * (((int64_t)g.C + bn - 1) / bn) + 7) / 8 * 8;
+  return grid >= (1 << 23) ? -1 : grid;
+}
+
 }  // namespace moe
