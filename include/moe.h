@@ -305,7 +305,8 @@ typedef enum {
   MOE_KERNEL_ROUTE = 11,       /* moe_route: top-K, weights, histograms, P sums
                                   (then META_SCAN and META_SCATTER, which also form the
                                   load-balancing loss) */
-  MOE_KERNEL_QUANT_ROWS = 12,    /* moe_quantize_rows */
+  MOE_KERNEL_QUANT_ROWS = 12,    /* moe_quantize_rows; moe_expert_forward_fp8 with few rows
+                                    per expert */
   MOE_KERNEL_QUANT_WEIGHTS = 13, /* moe_quantize_weights */
   MOE_KERNEL_RMSNORM = 14,       /* moe_rmsnorm_forward */
   MOE_KERNEL_RMSNORM_BWD = 15,   /* moe_rmsnorm_backward: dx and partial sums of dweight */

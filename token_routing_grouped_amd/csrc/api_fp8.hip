@@ -16,7 +16,7 @@ inline int32_t blocks(int32_t L) { return (L + MOE_QBLOCK - 1) / MOE_QBLOCK; }
 inline moe_status status_of(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
 
 struct Fp8Ws {
-  size_t aq, as, y, total;
+  size_t aq, as, y, af, total;
 };
 Fp8Ws fp8_layout(const moe_metadata *m, int32_t H, int32_t I) {
   const size_t cap = (size_t)m->capacity;
@@ -24,7 +24,11 @@ Fp8Ws fp8_layout(const moe_metadata *m, int32_t H, int32_t I) {
   w.aq = 0;
   w.as = w.aq + align_up(cap * (size_t)I);
   w.y = w.as + align_up(cap * (size_t)blocks(I));
-  w.total = w.y + align_up(cap * (size_t)H * 2);
+  w.af = w.y + align_up(cap * (size_t)H * 2);
+  Fp8Args g = {};
+  g.E = m->E;
+  g.cap = m->capacity;
+  w.total = w.af + (fp8_skinny(g) ? align_up(cap * (size_t)I * sizeof(float)) : 0);
   return w;
 }
 
@@ -136,7 +140,7 @@ moe_status moe_grouped_gemm_fp8(const moe_metadata *meta, const void *a, const v
   g.w_scale = w_scale;
   g.w_e8m0 = w_scale_type == MOE_SCALE_E8M0;
   g.out = (uint16_t *)out;
-  if (fp8_grid(false, g) < 0) return MOE_EUNSUPPORTED;
+  if (fp8_grid(g) < 0) return MOE_EUNSUPPORTED;
   hipStream_t st = (hipStream_t)stream;
   Bracket b(MOE_KERNEL_GROUPED_FP8, st);
   return status_of(launch_gemm_fp8(false, g, st));
@@ -179,6 +183,7 @@ moe_status moe_expert_forward_fp8(const moe_metadata *meta, const void *x, const
   up.out = (uint16_t *)h_save;
   up.aq = ws + L.aq;
   up.aq_scale = ws + L.as;
+  up.af = (float *)(ws + L.af);
   up.concat = layout == MOE_GATEUP_CONCAT;
   Fp8Args dn = fp8_args(meta, I, H);
   dn.a = up.aq;
@@ -189,10 +194,16 @@ moe_status moe_expert_forward_fp8(const moe_metadata *meta, const void *x, const
   dn.w_scale = w_down_scale;
   dn.w_e8m0 = up.w_e8m0;
   dn.out = (uint16_t *)(ws + L.y);
-  if (fp8_grid(true, up) < 0 || fp8_grid(false, dn) < 0) return MOE_EUNSUPPORTED;
+  if (fp8_grid(up) < 0 || fp8_grid(dn) < 0) return MOE_EUNSUPPORTED;
   if (meta->capacity > 0) {
     Bracket b(MOE_KERNEL_UP_SWIGLU_FP8, st);
     if (launch_gemm_fp8(true, up, st) != hipSuccess) return MOE_EHIP;
+  }
+  if (meta->capacity > 0 && fp8_skinny(up)) {  // rows past the last pair: never read
+    Bracket b(MOE_KERNEL_QUANT_ROWS, st);
+    if (launch_quantize_rows(up.af, meta->capacity, I, false, up.aq, up.aq_scale, 1, st) !=
+        hipSuccess)
+      return MOE_EHIP;
   }
   if (meta->capacity > 0) {
     Bracket b(MOE_KERNEL_DOWN_FP8, st);

@@ -500,12 +500,12 @@ hipError_t go(const Fp8Args &g, int64_t grid, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_gemm_fp8(bool swiglu, const Fp8Args &g, hipStream_t st) {
-  const int64_t grid = fp8_grid(swiglu, g);
+  const int64_t grid = fp8_grid(g);
   if (grid < 0) return hipErrorInvalidValue;
   if (grid == 0) return hipSuccess;
   int bt, bn;
-  fp8_tile(swiglu, g, &bt, &bn);
-  if (bt <= 64) return launch_gemm_fp8_skinny(swiglu, g, bt, grid, st);
+  fp8_tile(g, &bt, &bn);
+  if (fp8_skinny(g)) return launch_gemm_fp8_skinny(swiglu, g, bt, grid, st);
   const bool hw = g.a_e8m0 && g.w_e8m0;
   if (swiglu) return hw ? go<true, true>(g, grid, st) : go<false, true>(g, grid, st);
   return hw ? go<true, false>(g, grid, st) : go<false, false>(g, grid, st);

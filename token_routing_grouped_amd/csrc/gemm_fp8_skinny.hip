@@ -36,16 +36,16 @@ __device__ __forceinline__ float scale_value(const void *p, int e8m0, int64_t i)
   return e8m0 ? exponent_value(((const uint8_t *)p)[i]) : ((const float *)p)[i];
 }
 
-constexpr int kSB = 64;  // blocks of K whose scales LDS holds at a time
+constexpr int kSB = 48;  // blocks of K whose scales LDS holds at a time
 
-// TT: 16-row pieces of a tile; NW: waves, 32 columns each; U: blocks of weights in flight
-template <bool SWI, int TT, int NW, int U>
-__global__ __launch_bounds__(64 * NW, TT > 2 ? 2 : 4) void skinny_kernel(Fp8Args g) {
-  constexpr int NT = 64 * NW, BT = 16 * TT, BN = 32 * NW, TN = 2;
-  static_assert(!SWI || BN == 256, "a SwiGLU tile holds one block of 128 pairs");
+// TT: 16-row pieces of a tile; NW: waves, TN 16-column pieces each; U: blocks in flight (of
+// both operands: loads are waited for in the order of their issue, so rows fetched later than
+// the weights ahead of them would hold those back); OCC: waves per SIMD
+template <bool SWI, int TT, int TN, int NW, int U, int OCC>
+__global__ __launch_bounds__(64 * NW, OCC) void skinny_kernel(Fp8Args g) {
+  constexpr int NT = 64 * NW, BT = 16 * TT, BN = 16 * TN * NW;
   __shared__ float s_sa[kSB][BT];           // row scales
   __shared__ f32x2 s_sw[kSB][BN / 16];      // weight scales of a 16-column piece's even and odd rows
-  __shared__ uint32_t s_max[SWI ? NW : 1][BT];
   __shared__ int s_tab[2 * (MOE_MAX_EXPERTS + 1)];
   int *s_pref = s_tab, *s_off = s_tab + MOE_MAX_EXPERTS + 1;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -100,9 +100,7 @@ __global__ __launch_bounds__(64 * NW, TT > 2 ? 2 : 4) void skinny_kernel(Fp8Args
   const uint8_t *pw[TN], *pa[TT];
 #pragma unroll
   for (int n = 0; n < TN; n++)
-    pw[n] = g.w + ((int64_t)e * g.C + w_row(wave * 32 + n * 16 + fr)) * g.K;
-#pragma unroll
-  for (int t = 0; t < TT; t++) pa[t] = g.a + a_row(t * 16 + fr) * g.K;
+    pw[n] = g.w + ((int64_t)e * g.C + w_row((wave * TN + n) * 16 + fr)) * g.K;
 
   // a block's two chunks of a row; past K (in the last block) the row's last chunk again,
   // which the rows' operand then cancels
@@ -111,13 +109,18 @@ __global__ __launch_bounds__(64 * NW, TT > 2 ? 2 : 4) void skinny_kernel(Fp8Args
     v[0] = *(const u32x4 *)(p + min(k, g.K - 16));
     v[1] = *(const u32x4 *)(p + min(k + 64, g.K - 16));
   };
-  u32x4 w[U][TN][2], a[2][TT][2];
+  u32x4 w[U][TN][2], a[U][TT][2];
+  // the weights first: their addresses need no row map
 #pragma unroll
   for (int u = 0; u < U; u++)
 #pragma unroll
     for (int n = 0; n < TN; n++) at(pw[n], u, w[u][n]);
 #pragma unroll
-  for (int t = 0; t < TT; t++) at(pa[t], 0, a[0][t]);
+  for (int t = 0; t < TT; t++) pa[t] = g.a + a_row(t * 16 + fr) * g.K;
+#pragma unroll
+  for (int u = 0; u < U; u++)
+#pragma unroll
+    for (int t = 0; t < TT; t++) at(pa[t], u, a[u][t]);
 
   f32x4 acc[TN][TT];
 #pragma unroll
@@ -125,7 +128,7 @@ __global__ __launch_bounds__(64 * NW, TT > 2 ? 2 : 4) void skinny_kernel(Fp8Args
 #pragma unroll
     for (int t = 0; t < TT; t++) acc[n][t] = f32x4{0, 0, 0, 0};
 
-  static_assert(U % 2 == 0 && kSB % U == 0, "the rows' two sets take turns");
+  static_assert(kSB % U == 0, "the sets' order holds over the scales' chunks");
   for (int kc = 0; kc < nk; kc += kSB) {
     if (kc > 0) __syncthreads();
     for (int i = tid; i < kSB * BT; i += NT) {
@@ -146,14 +149,12 @@ __global__ __launch_bounds__(64 * NW, TT > 2 ? 2 : 4) void skinny_kernel(Fp8Args
       for (int u = 0; u < U; u++) {
         const int kb = k0 + u;
         if (kb >= end) break;  // uniform
-#pragma unroll
-        for (int t = 0; t < TT; t++) at(pa[t], kb + 1, a[(u + 1) & 1][t]);
         if ((kb + 1) * kQB > g.K) {  // chunks past K
           const int k = kb * kQB + fg * 16;
 #pragma unroll
           for (int t = 0; t < TT; t++) {
-            if (k >= g.K) a[u & 1][t][0] = u32x4{0, 0, 0, 0};
-            if (k + 64 >= g.K) a[u & 1][t][1] = u32x4{0, 0, 0, 0};
+            if (k >= g.K) a[u][t][0] = u32x4{0, 0, 0, 0};
+            if (k + 64 >= g.K) a[u][t][1] = u32x4{0, 0, 0, 0};
           }
         }
         f32x4 d[TN][TT];
@@ -162,7 +163,7 @@ __global__ __launch_bounds__(64 * NW, TT > 2 ? 2 : 4) void skinny_kernel(Fp8Args
           bf16x8 bt[TT];
 #pragma unroll
           for (int t = 0; t < TT; t++) {
-            const u32x4 v = a[u & 1][t][q >> 1];
+            const u32x4 v = a[u][t][q >> 1];
             bt[t] = (q & 1) ? widen(v[2], v[3]) : widen(v[0], v[1]);
           }
 #pragma unroll
@@ -176,6 +177,8 @@ __global__ __launch_bounds__(64 * NW, TT > 2 ? 2 : 4) void skinny_kernel(Fp8Args
           }
         }
 #pragma unroll
+        for (int t = 0; t < TT; t++) at(pa[t], kb + U, a[u][t]);
+#pragma unroll
         for (int n = 0; n < TN; n++) at(pw[n], kb + U, w[u][n]);
         const int k = kb - kc;
 #pragma unroll
@@ -183,7 +186,7 @@ __global__ __launch_bounds__(64 * NW, TT > 2 ? 2 : 4) void skinny_kernel(Fp8Args
           const float sa = s_sa[k][t * 16 + fr];
 #pragma unroll
           for (int n = 0; n < TN; n++) {
-            const f32x2 sw = s_sw[k][wave * 2 + n];
+            const f32x2 sw = s_sw[k][wave * TN + n];
             const float x0 = sa * sw[0], x1 = sa * sw[1];
             acc[n][t][0] += d[n][t][0] * x0;
             acc[n][t][1] += d[n][t][1] * x1;
@@ -201,69 +204,31 @@ __global__ __launch_bounds__(64 * NW, TT > 2 ? 2 : 4) void skinny_kernel(Fp8Args
 #pragma unroll
     for (int t = 0; t < TT; t++) asm volatile("" : "+v"(acc[n][t]));
 
-  // ---- epilogues: acc[n][t] of lane l holds columns 16 n + 4 (l / 16) .. + 3 of the wave's
-  // 32 and row 16 t + l % 16
-  float av[TN][TT][2];
+  // ---- epilogue: acc[n][t] of lane l holds columns 16 n + 4 (l / 16) .. + 3 of the wave's and
+  // row 16 t + l % 16. SwiGLU: a in fp32, which a pass of its own puts in 8 bits (a tile of
+  // one block of 128 pairs would be twice as wide, too few tiles for the chip to share evenly).
 #pragma unroll
   for (int t = 0; t < TT; t++) {
     const int tok = t * 16 + fr;
-    uint32_t m = 0;
+    if (tok >= rows) continue;
+    const int64_t s = row0 + tok;
 #pragma unroll
     for (int n = 0; n < TN; n++) {
-      const int c = nt * BN + wave * 32 + n * 16 + fg * 4;
+      const int c = nt * BN + (wave * TN + n) * 16 + fg * 4;
+      if (c >= g.C) continue;
       const f32x4 v = acc[n][t];
-      if (g.out && tok < rows && c < g.C)
-        *(u32x2 *)(g.out + (int64_t)(row0 + tok) * g.C + c) =
-            u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-      if constexpr (SWI) {
-#pragma unroll
-        for (int p = 0; p < 2; p++) {
-          const float y = silu_fast(v[2 * p]) * v[2 * p + 1];
-          const uint32_t b = finite_abs_bits(y);
-          av[n][t][p] = y;
-          m = c < g.C && b > m ? b : m;
-        }
-      }
-    }
-    if constexpr (SWI) {
-#pragma unroll
-      for (int s = 16; s < 64; s <<= 1) {
-        const uint32_t u = (uint32_t)__shfl_xor((int)m, s, kWave);
-        m = m > u ? m : u;
-      }
-      if (fg == 0) s_max[wave][tok] = m;
-    }
-  }
-  if constexpr (SWI) {
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < TT; t++) {
-      const int tok = t * 16 + fr;
-      uint32_t m = s_max[0][tok];
-#pragma unroll
-      for (int i = 1; i < NW; i++) m = m > s_max[i][tok] ? m : s_max[i][tok];
-      const uint32_t ex = scale_exponent(m);
-      const float inv = exponent_inverse(ex);
-      const uint32_t q = pack_e4m3(to_q(av[0][t][0], inv), to_q(av[0][t][1], inv),
-                                   to_q(av[1][t][0], inv), to_q(av[1][t][1], inv));
-      if (tok < rows) {
-        const int64_t s = row0 + tok;
-#pragma unroll
-        for (int n = 0; n < TN; n++) {
-          const int j = nt * kQB + wave * 16 + n * 8 + fg * 2;
-          if (j < I) *(uint16_t *)(g.aq + s * I + j) = (uint16_t)(q >> (16 * n));
-        }
-        if (wave == 0 && fg == 0)
-          g.aq_scale[s * ((I + kQB - 1) / kQB) + nt] = (uint8_t)ex;
-      }
+      if (g.out)
+        *(u32x2 *)(g.out + s * g.C + c) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      if constexpr (SWI)
+        *(f32x2 *)(g.af + s * I + (c >> 1)) = f32x2{silu_fast(v[0]) * v[1], silu_fast(v[2]) * v[3]};
     }
   }
 }
 
-template <bool SWI, int TT, int U>
+template <bool SWI, int TT, int TN, int NW, int U, int OCC>
 hipError_t go(const Fp8Args &g, int64_t grid, hipStream_t st) {
-  constexpr int NW = SWI ? 8 : 4;
-  hipLaunchKernelGGL((skinny_kernel<SWI, TT, NW, U>), dim3((uint32_t)grid), dim3(64 * NW), 0, st, g);
+  hipLaunchKernelGGL((skinny_kernel<SWI, TT, TN, NW, U, OCC>), dim3((uint32_t)grid), dim3(64 * NW), 0,
+                     st, g);
   return hipGetLastError();
 }
 
@@ -271,11 +236,8 @@ hipError_t go(const Fp8Args &g, int64_t grid, hipStream_t st) {
 
 hipError_t launch_gemm_fp8_skinny(bool swiglu, const Fp8Args &g, int bt, int64_t grid,
                                   hipStream_t st) {
-  if (swiglu)
-    return bt == 16 ? go<true, 1, 4>(g, grid, st)
-                    : bt == 32 ? go<true, 2, 2>(g, grid, st) : go<true, 4, 4>(g, grid, st);
-  return bt == 16 ? go<false, 1, 4>(g, grid, st)
-                  : bt == 32 ? go<false, 2, 2>(g, grid, st) : go<false, 4, 4>(g, grid, st);
+  if (swiglu) return bt == 16 ? go<true, 1, 2, 4, 2, 5>(g, grid, st) : go<true, 2, 2, 4, 2, 3>(g, grid, st);
+  return bt == 16 ? go<false, 1, 2, 4, 2, 5>(g, grid, st) : go<false, 2, 2, 4, 2, 3>(g, grid, st);
 }
 
 }  // namespace moe

@@ -197,11 +197,13 @@ struct Fp8Args {
   // SwiGLU: C = 2I; a = silu(gate) up in e4m3 [cap,I] with e8m0 scales [cap, ceil(I/128)]
   uint8_t *aq;
   uint8_t *aq_scale;
+  float *af;   // few rows per expert: a in fp32 [cap,I] instead, put in 8 bits by its own pass
   int concat;  // rows of w (and its scale blocks) are [gates | ups]
 };
-// rows and columns of a tile, and the workgroups of a launch (-1: too many)
-void fp8_tile(bool swiglu, const Fp8Args &g, int *bt, int *bn);
-int64_t fp8_grid(bool swiglu, const Fp8Args &g);
+// whether the products take the kernel for few rows per expert, rows and columns of a tile, and the workgroups of a launch (-1: too many)
+bool fp8_skinny(const Fp8Args &g);
+void fp8_tile(const Fp8Args &g, int *bt, int *bn);
+int64_t fp8_grid(const Fp8Args &g);
 hipError_t launch_gemm_fp8_skinny(bool swiglu, const Fp8Args &g, int bt, int64_t grid,
                                   hipStream_t st);
 hipError_t launch_gemm_fp8(bool swiglu, const Fp8Args &g, hipStream_t st);
