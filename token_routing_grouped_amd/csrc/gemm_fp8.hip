@@ -309,6 +309,10 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
 #pragma unroll
   for (int n = 0; n < TN; n++) weights_piece(0, n);
   tokens_piece(0, 0);
+  auto other_of = [&](uint32_t s) { return s ^ (lds0 ^ (lds0 + STAGE)); };
+  constexpr int EARLY = (LA + LB) / 2;  // loads made in a step's last pieces; the others in the
+                                        // first pieces of the next
+  static_assert(LA + LB - EARLY == 4, "two in each of two pieces");
   uint32_t stage = lds0;  // of the block being multiplied
   int set = 0;            // its scales' set
   // Tokens past the segment repeat its first row, operands and scales, so they may store its
@@ -358,7 +362,10 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
       if (t + 1 == TT - 3) tokens_piece(si, TT - 2);
       if (t == TT - 3) tokens_piece(si, TT - 1);
 #pragma unroll
-      for (int n = 0; n < TN; n++) multiply(n, t);
+      for (int n = 0; n < TN; n++) {
+        multiply(n, t);
+        if (t < 2 && n % 2 == 1 && kb > 0) load(other_of(stage), EARLY + t * 2 + n / 2);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     // after an epilogue whose stores are all issued: not for those, only for the loads ahead
@@ -367,7 +374,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
     else wait_loads();
     if (last) put_scales(set ^ 1);
     __syncthreads();
-    const uint32_t other = stage ^ (lds0 ^ (lds0 + STAGE)), d = other - stage;
+    const uint32_t other = other_of(stage), d = other - stage;
     ta0 += d;
     ta1 += d;
     wa0 += d;
@@ -384,8 +391,12 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
       weights_piece(sj, n);
       if (n == 0) tokens_next(sj);
 #pragma unroll
-      for (int i = n * (LA + LB) / TN; i < (n + 1) * (LA + LB) / TN; i++) load(stage, i);
+      for (int i = n * EARLY / TN; i < (n + 1) * EARLY / TN; i++) load(stage, i);
       __builtin_amdgcn_sched_barrier(0);
+    }
+    if (kb + 1 == nk) {  // before the epilogue's stores
+#pragma unroll
+      for (int i = EARLY; i < LA + LB; i++) load(stage, i);
     }
     stage = other;
     if (last) set ^= 1;
