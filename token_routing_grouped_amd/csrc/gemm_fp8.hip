@@ -86,9 +86,9 @@ __device__ __forceinline__ u32x2 to_bf16(const f32x4 &v) {
   return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
-// WT x WN waves. HW: both scales are e8m0. FAR: rows are found by 64-bit addresses per lane and
-// chunks past K come from a page of zeros; else (K in whole blocks, each operand's bytes
-// counted in 32 bits) by a uniform address that moves along K and a fixed offset per lane.
+// WT x WN waves. HW: both scales are e8m0. FAR: rows are found by 64-bit addresses per lane,
+// chunks past K come from a page of zeros, and every column piece has scales of its own; else
+// (K in whole blocks, each operand's bytes counted in 32 bits) by a uniform address that moves along K and a fixed offset per lane.
 template <bool HW, bool SWI, bool FAR, int BT, int BN, int WT, int WN>
 __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   constexpr int NT = 64 * WT * WN, NW = WT * WN;
@@ -269,12 +269,25 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
     return *(const __attribute__((address_space(3))) uint32_t *)(uintptr_t)a;
   };
   i32x8 an[TN], bt[3];  // tokens' pieces: t in bt[t % 3]
-  uint32_t sn[TN][HW ? 1 : 2], sa[3];
+  // Scales of the weights' pieces: of a lane's row (HW), or of even and odd rows. All pieces of
+  // a wave lie in the same blocks of 128 rows, but for gates and ups one after the other where
+  // I is no multiple of 128 (FAR).
+  constexpr int NS = FAR ? TN : 1;
+  uint32_t sn[NS][2], sx[NS][2], sa[3];  // sx: the next block's
   auto weights_piece = [&](int si, int n) {  // si: the block's place among the scales in LDS
     an[n] = pair(wa0, wa1, n * 16 * kQB);
-    const uint32_t p = lw + si * (F * 8) + n * 8;
-    sn[n][0] = word(p);
-    if constexpr (!HW) sn[n][1] = word(p + 4);
+    if (n < NS) {
+      const uint32_t p = lw + si * (F * 8) + n * 8;
+      sx[n][0] = word(p);
+      if constexpr (!HW) sx[n][1] = word(p + 4);
+    }
+  };
+  auto next_scales = [&] {
+#pragma unroll
+    for (int n = 0; n < NS; n++) {
+      sn[n][0] = sx[n][0];
+      sn[n][1] = sx[n][1];
+    }
   };
   auto tokens_piece = [&](int si, int t) {
     bt[t % 3] = pair(ta0, ta1, t * 16 * kQB);
@@ -308,6 +321,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   __syncthreads();
 #pragma unroll
   for (int n = 0; n < TN; n++) weights_piece(0, n);
+  next_scales();
   tokens_piece(0, 0);
   auto other_of = [&](uint32_t s) { return s ^ (lds0 ^ (lds0 + STAGE)); };
   constexpr int EARLY = (LA + LB) / 2;  // loads made in a step's last pieces; the others in the
@@ -329,24 +343,37 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   for (int n = 0; n < TN; n++)
 #pragma unroll
     for (int t = 0; t < TT; t++) acc[n][t] = f32x4{0, 0, 0, 0};
-  auto multiply = [&](int n, int t) {
-    if constexpr (HW) {
-      acc[n][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-          an[n], bt[t % 3], acc[n][t], 0, 0, 0, (int)sn[n][0], 0, (int)sa[t % 3]);
-    } else {
-      const f32x4 z = {0, 0, 0, 0};
-      const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-          an[n], bt[t % 3], z, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
-      const float x0 = __uint_as_float(sa[t % 3]) * __uint_as_float(sn[n][0]);
-      const float x1 = __uint_as_float(sa[t % 3]) * __uint_as_float(sn[n][1]);
+  // The products of pieces n and t. fp32 scales: a block's sums d are multiplied and added one
+  // product later, when the matrix instruction is done.
+  f32x4 d;
+  float x0 = 0.0f, x1 = 0.0f;
+  auto add = [&](int n, int t) {
+    if constexpr (!HW) {
       acc[n][t][0] += d[0] * x0;
       acc[n][t][1] += d[1] * x1;
       acc[n][t][2] += d[2] * x0;
       acc[n][t][3] += d[3] * x1;
+      asm volatile("" : "+v"(acc[n][t]));
     }
-    // pinned to this place: the compiler would gather the products behind the barrier, and
-    // hold all their operands until then
-    asm volatile("" : "+v"(acc[n][t]));
+  };
+  auto multiply = [&](int n, int t, int pn, int pt) {  // pn, pt: the product before, if >= 0
+    const int m = FAR ? n : 0;
+    if constexpr (HW) {
+      acc[n][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+          an[n], bt[t % 3], acc[n][t], 0, 0, 0, (int)sn[m][0], 0, (int)sa[t % 3]);
+      // pinned to this place: the compiler would gather the products behind the barrier, and
+      // hold all their operands until then
+      asm volatile("" : "+v"(acc[n][t]));
+    } else {
+      const f32x4 z = {0, 0, 0, 0};
+      f32x4 e_ = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+          an[n], bt[t % 3], z, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+      asm volatile("" : "+v"(e_));
+      if (pn >= 0) add(pn, pt);
+      d = e_;
+      x0 = __uint_as_float(sa[t % 3]) * __uint_as_float(sn[m][0]);
+      x1 = SWI || FAR ? __uint_as_float(sa[t % 3]) * __uint_as_float(sn[m][1]) : x0;
+    }
   };
   for (int kb = 0; kb < nk; kb++) {
     const int k = kb % kKC, len = min(kKC, nk - (kb - k));
@@ -363,7 +390,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
       if (t == TT - 3) tokens_piece(si, TT - 1);
 #pragma unroll
       for (int n = 0; n < TN; n++) {
-        multiply(n, t);
+        multiply(n, t, n ? n - 1 : t ? TN - 1 : -1, n ? t : t - 1);
         if (t < 2 && n % 2 == 1 && kb > 0) load(other_of(stage), EARLY + t * 2 + n / 2);
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -386,14 +413,16 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int n = 0; n < TN; n++) {
-      multiply(n, TT - 2);
-      multiply(n, TT - 1);
+      multiply(n, TT - 2, n ? n - 1 : TN - 1, n ? TT - 1 : TT - 3);
+      multiply(n, TT - 1, n, TT - 2);
       weights_piece(sj, n);
       if (n == 0) tokens_next(sj);
 #pragma unroll
       for (int i = n * EARLY / TN; i < (n + 1) * EARLY / TN; i++) load(stage, i);
       __builtin_amdgcn_sched_barrier(0);
     }
+    add(TN - 1, TT - 1);
+    next_scales();
     if (kb + 1 == nk) {  // before the epilogue's stores
 #pragma unroll
       for (int i = EARLY; i < LA + LB; i++) load(stage, i);
@@ -503,7 +532,7 @@ hipError_t go(const Fp8Args &g, int64_t grid, hipStream_t st) {
 }
 template <bool HW, bool SWI>
 hipError_t go(const Fp8Args &g, int64_t grid, hipStream_t st) {
-  const bool near = g.K % kQB == 0 && g.nbk > 1 && (int64_t)g.a_span * g.K <= 0xffffffffll &&
+  const bool near = g.K % kQB == 0 && g.nbk > 1 && !(g.concat && g.C / 2 % kQB) && (int64_t)g.a_span * g.K <= 0xffffffffll &&
                     (int64_t)g.C * g.K <= 0xffffffffll;
   return near ? go<HW, SWI, false>(g, grid, st) : go<HW, SWI, true>(g, grid, st);
 }
