@@ -100,7 +100,7 @@ def test_expert_forward_refusals():
     f, ws = L().moe_expert_forward_fp8, L().moe_expert_forward_fp8_workspace
     need = ws(meta(), 64, 32)
     assert need == 256 + 256 + 8 * 64 * 2 + 8 * 32 * 4
-    assert ws(meta(cap=61), 64, 32) == 2048 + 256 + 61 * 64 * 2 + 128
+    assert ws(meta(cap=61), 64, 32) == 2048 + 256 + 61 * 64 * 2 + 128 + 256
 
     def call(m=None, x=A, xs=A, tx=0, u=A, us=A, d=A, ds=A, tw=0, H=64, I=32, lay=0, out=A, wk=A, nb=need):
         return f(meta() if m is None else m, x, xs, tx, u, us, d, ds, tw, H, I, lay, None, out, wk, nb, None)

@@ -16,7 +16,7 @@ inline int32_t blocks(int32_t L) { return (L + MOE_QBLOCK - 1) / MOE_QBLOCK; }
 inline moe_status status_of(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
 
 struct Fp8Ws {
-  size_t aq, as, y, af, total;
+  size_t aq, as, y, ys, af, total;
 };
 Fp8Ws fp8_layout(const moe_metadata *m, int32_t H, int32_t I) {
   const size_t cap = (size_t)m->capacity;
@@ -24,11 +24,13 @@ Fp8Ws fp8_layout(const moe_metadata *m, int32_t H, int32_t I) {
   w.aq = 0;
   w.as = w.aq + align_up(cap * (size_t)I);
   w.y = w.as + align_up(cap * (size_t)blocks(I));
-  w.af = w.y + align_up(cap * (size_t)H * 2);
   Fp8Args g = {};
   g.E = m->E;
   g.cap = m->capacity;
-  w.total = w.af + (fp8_skinny(g) ? align_up(cap * (size_t)I * sizeof(float)) : 0);
+  const bool skinny = fp8_skinny(g);  // a in fp32 first; else scales of y
+  w.ys = w.y + align_up(cap * (size_t)H * 2);
+  w.af = w.ys + (skinny ? 0 : align_up(cap * (size_t)((H + kYCols - 1) / kYCols)));
+  w.total = w.af + (skinny ? align_up(cap * (size_t)I * sizeof(float)) : 0);
   return w;
 }
 
@@ -194,6 +196,7 @@ moe_status moe_expert_forward_fp8(const moe_metadata *meta, const void *x, const
   dn.w_scale = w_down_scale;
   dn.w_e8m0 = up.w_e8m0;
   dn.out = (uint16_t *)(ws + L.y);
+  dn.ys = fp8_skinny(dn) ? nullptr : ws + L.ys;
   if (fp8_grid(up) < 0 || fp8_grid(dn) < 0) return MOE_EUNSUPPORTED;
   if (meta->capacity > 0) {
     Bracket b(MOE_KERNEL_UP_SWIGLU_FP8, st);
@@ -210,9 +213,12 @@ moe_status moe_expert_forward_fp8(const moe_metadata *meta, const void *x, const
     if (launch_gemm_fp8(false, dn, st) != hipSuccess) return MOE_EHIP;
   }
   Bracket b(MOE_KERNEL_COMBINE, st);
-  return status_of(launch_combine(true, dn.out, meta->num_activated_expert_per_token_offset,
-                                  meta->s_reverse_scatter_idx, meta->router_scores, meta->N, H,
-                                  meta->capacity, out, st));
+  const int32_t *off = meta->num_activated_expert_per_token_offset;
+  const int32_t *rev = meta->s_reverse_scatter_idx;
+  return status_of(dn.ys ? launch_combine_f16(dn.out, dn.ys, off, rev, meta->router_scores, meta->N, H,
+                                              meta->capacity, out, st)
+                         : launch_combine(true, dn.out, off, rev, meta->router_scores, meta->N, H,
+                                          meta->capacity, out, st));
 }
 
 }  // extern "C"

@@ -15,6 +15,8 @@
 // of a valid expert id is the token's (number of valid slots before k)-th pair,
 // and its gradient is the sum, in tile order, of the per-column-tile partials the
 // down-projection backward wrote for that pair.
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 
@@ -57,6 +59,25 @@ struct Vec<float> {  // fp32: 4 elements per 16 bytes
   }
 };
 
+struct F16 {  // fp16 with a scale per row and kYCols columns, rounded to bf16 at the end
+  uint16_t v;
+};
+template <>
+struct Vec<F16> {
+  static constexpr int n = 8;
+  __device__ static void add(const u32x4 &v, float w, float *f) {
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const uint32_t x = v[i];  // (a bit cast of the element itself reads element 0)
+      const f16x2 h = __builtin_bit_cast(f16x2, x);
+      f[2 * i] += w * (float)h[0];
+      f[2 * i + 1] += w * (float)h[1];
+    }
+  }
+  __device__ static u32x4 pack(const float *f) { return Vec<uint16_t>::pack(f); }
+};
+
 struct DscoreArgs {
   const int32_t *topk_idx;
   int K, E;
@@ -73,8 +94,11 @@ __global__ __launch_bounds__(CT) void combine_kernel(const T *__restrict__ y,
                                                     const int32_t *__restrict__ s_rev,
                                                     const float *__restrict__ scores, int N,
                                                     int H, int cap, T *__restrict__ out,
-                                                    DscoreArgs ds) {
+                                                    DscoreArgs ds,
+                                                    const uint8_t *__restrict__ ys = nullptr) {
   constexpr int V = Vec<T>::n;
+  constexpr bool SCALED = std::is_same<T, F16>::value;
+  const int nys = (H + kYCols - 1) / kYCols;
   const int lane = threadIdx.x & 63;
   const int t = blockIdx.x * (CT / 64) + (threadIdx.x >> 6);
   if (t >= N) return;
@@ -96,6 +120,7 @@ __global__ __launch_bounds__(CT) void combine_kernel(const T *__restrict__ y,
     for (int j0 = 0; j0 < n; j0 += PAIRS) {
       u32x4 raw[PAIRS][CHUNKS];
       float w[PAIRS];
+      uint32_t ex[PAIRS][SCALED ? CHUNKS : 1];
 #pragma unroll
       for (int p = 0; p < PAIRS; p++) {
         const int j = j0 + p < n ? j0 + p : j0;  // a missing second pair re-reads the first
@@ -106,6 +131,8 @@ __global__ __launch_bounds__(CT) void combine_kernel(const T *__restrict__ y,
         for (int i = 0; i < CHUNKS; i++) {
           const int c = c0 + i * 64 + lane;
           raw[p][i] = c < nchunk ? yrow[c] : u32x4{0, 0, 0, 0};
+          if constexpr (SCALED)
+            ex[p][i] = ys[(int64_t)s * nys + (c < nchunk ? c : nchunk - 1) / (kYCols / V)];
         }
       }
       // ascending pair order within and across groups
@@ -113,7 +140,9 @@ __global__ __launch_bounds__(CT) void combine_kernel(const T *__restrict__ y,
       for (int p = 0; p < PAIRS; p++) {
         if (j0 + p >= n) break;  // wave-uniform
 #pragma unroll
-        for (int i = 0; i < CHUNKS; i++) Vec<T>::add(raw[p][i], w[p], acc[i]);
+        for (int i = 0; i < CHUNKS; i++)
+          Vec<T>::add(raw[p][i],
+                      SCALED ? w[p] * __uint_as_float((ex[p][i] - 14u) << 23) : w[p], acc[i]);
       }
     }
 #pragma unroll
@@ -147,10 +176,12 @@ hipError_t launch_t(const void *y, const int32_t *tok_off, const int32_t *s_rev,
     constexpr int CH = 1;  // one chunk per lane: a column block is 64 chunks
     const int nblk = (H / Vec<T>::n + 64 * CH - 1) / (64 * CH);
     hipLaunchKernelGGL((combine_kernel<T, DSCORE, CH, 8>), dim3(grid, nblk), dim3(CT), 0, stream,
-                       (const T *)y, tok_off, s_rev, scores, N, H, cap, (T *)out, ds);
+                       (const T *)y, tok_off, s_rev, scores, N, H, cap, (T *)out, ds,
+                       (const uint8_t *)nullptr);
   } else {
     hipLaunchKernelGGL((combine_kernel<T, DSCORE, 4, 2>), dim3(grid), dim3(CT), 0, stream,
-                       (const T *)y, tok_off, s_rev, scores, N, H, cap, (T *)out, ds);
+                       (const T *)y, tok_off, s_rev, scores, N, H, cap, (T *)out, ds,
+                       (const uint8_t *)nullptr);
   }
   return hipGetLastError();
 }
@@ -172,6 +203,22 @@ hipError_t launch_combine(bool bf16, const void *y, const int32_t *tok_off, cons
   if (N == 0) return hipSuccess;
   DscoreArgs ds = {};
   return launch<false>(bf16, y, tok_off, s_rev, scores, N, H, cap, out, ds, stream);
+}
+
+hipError_t launch_combine_f16(const void *y, const uint8_t *ys, const int32_t *tok_off,
+                              const int32_t *s_rev, const float *scores, int N, int H, int cap,
+                              void *out, hipStream_t stream) {
+  if (N == 0) return hipSuccess;
+  const int grid = (N + 3) / 4;
+  if (N < kSplitTokens)
+    hipLaunchKernelGGL((combine_kernel<F16, false, 1, 8>), dim3(grid, (H / 8 + 63) / 64), dim3(CT), 0,
+                       stream, (const F16 *)y, tok_off, s_rev, scores, N, H, cap, (F16 *)out,
+                       DscoreArgs{}, ys);
+  else
+    hipLaunchKernelGGL((combine_kernel<F16, false, 4, 2>), dim3(grid), dim3(CT), 0, stream,
+                       (const F16 *)y, tok_off, s_rev, scores, N, H, cap, (F16 *)out, DscoreArgs{},
+                       ys);
+  return hipGetLastError();
 }
 
 hipError_t launch_combine_dscore(bool bf16, const void *dxg, const int32_t *tok_off,

@@ -37,6 +37,12 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
 }
 
+// biased exponent (15..254) of the largest finite |y| of a row's columns that share a scale:
+// y is kept as fp16 of y 2^(141 - e), at most 2^15
+__device__ __forceinline__ uint32_t y_exponent(uint32_t amax_bits) {
+  const uint32_t e = amax_bits >> 23;
+  return e < 15u ? 15u : e;
+}
 // maximum over each row of 16 lanes (DPP row_ror 8, 4, 2, 1); all lanes active
 __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
 #define MOE_ROR(N)                                                                            \

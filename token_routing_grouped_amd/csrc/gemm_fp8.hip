@@ -85,6 +85,11 @@ __device__ __forceinline__ u32x4 columns8(u32x2 a, u32x2 b) {
 __device__ __forceinline__ u32x2 to_bf16(const f32x4 &v) {
   return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
+__device__ __forceinline__ u32x2 to_f16(const f32x4 &v, float by) {
+  typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(u32x2, f16x4{(_Float16)(v[0] * by), (_Float16)(v[1] * by),
+                                         (_Float16)(v[2] * by), (_Float16)(v[3] * by)});
+}
 
 // WT x WN waves. HW: both scales are e8m0. FAR: rows are found by 64-bit addresses per lane,
 // chunks past K come from a page of zeros, and every column piece has scales of its own; else
@@ -437,13 +442,40 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   const int nt = tile.nt, row0 = tile.row0, rows = tile.rows;
   // ---- epilogues: acc[n][t] of lane l holds columns 16 n + 4 (l / 16) .. + 3 of token
   // 16 t + l % 16 of its wave
-  // bf16 rows of piece t, two column pieces at a time
+  // Rows of piece t in 16 bits, two column pieces at a time: bf16; or, for the combine, fp16
+  // with a power of two for the wave's 64 columns of a row, which puts their largest at
+  // 2^14 .. 2^15. fp16 keeps three bits more, so that the sum's one rounding to bf16 counts.
+  static_assert(SWI || BN / WN == kYCols, "one scale per wave and row");
   auto store_rows = [&](int t) {
     const int tok = wt * (BT / WT) + t * 16 + fr;
-    uint16_t *o = g.out + (int64_t)(row0 + (tok < rows ? tok : 0)) * g.C;
+    const int64_t s = row0 + (tok < rows ? tok : 0);
+    uint16_t *o = g.out + s * g.C;
+    float by = 1.0f;
+    if (!SWI && g.ys) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int n = 0; n < TN; n++) {
+        const bool in = nt * BN + wn * (BN / WN) + n * 16 + fg * 4 < g.C;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const uint32_t b = finite_abs_bits(acc[n][t][i]);
+          m = in && b > m ? b : m;
+        }
+      }
+#pragma unroll
+      for (int h = 16; h < 64; h <<= 1) {
+        const uint32_t u = (uint32_t)__shfl_xor((int)m, h, kWave);
+        m = m > u ? m : u;
+      }
+      const uint32_t ex = y_exponent(m);
+      by = __uint_as_float((268u - ex) << 23);
+      const int c0 = nt * BN + wn * (BN / WN);
+      if (fg == 0 && c0 < g.C) g.ys[s * ((g.C + kYCols - 1) / kYCols) + c0 / kYCols] = (uint8_t)ex;
+    }
 #pragma unroll
     for (int n = 0; n < TN; n += 2) {
-      const u32x4 v = columns8(to_bf16(acc[n][t]), to_bf16(acc[n + 1][t]));
+      const u32x4 v = !SWI && g.ys ? columns8(to_f16(acc[n][t], by), to_f16(acc[n + 1][t], by))
+                                   : columns8(to_bf16(acc[n][t]), to_bf16(acc[n + 1][t]));
       const int c = nt * BN + wn * (BN / WN) + n * 16 + fg * 8;
       if (even || (tok < rows && c < g.C)) *(u32x4 *)(o + c) = v;
     }

@@ -151,6 +151,11 @@ hipError_t launch_gemm_f32(GemmKind kind, const GemmArgs &g, hipStream_t stream)
 hipError_t launch_combine(bool bf16, const void *y, const int32_t *tok_off,
                           const int32_t *s_rev, const float *scores, int N, int H, int cap,
                           void *out, hipStream_t stream);
+// The same from fp16 y with a scale per row and kYCols columns (its exponent e: y stands for
+// y 2^(e - 141)), to bf16.
+hipError_t launch_combine_f16(const void *y, const uint8_t *ys, const int32_t *tok_off,
+                              const int32_t *s_rev, const float *scores, int N, int H, int cap,
+                              void *out, hipStream_t stream);
 // The same for dx with unit weights, also writing d_topk_weights[t,k] = the sum over
 // column tiles of partial[s_rev[q],tile] for the slot's pair q (0 at invalid slots).
 hipError_t launch_combine_dscore(bool bf16, const void *dxg, const int32_t *tok_off,
@@ -181,6 +186,7 @@ hipError_t launch_rmsnorm_dw(const float *part, int N, int H, bool bf16, void *d
 
 // Grouped products: out[s,:] = a[row(s),:] W_e^T over e4m3 operands, both [.., K]
 // reduction-contiguous, with a scale per row and 128 (a) and per 128 x 128 (w).
+constexpr int kYCols = 64;  // columns of y that share a scale
 struct Fp8Args {
   const int32_t *foff;  // [E+1]
   int E, cap;
@@ -194,6 +200,7 @@ struct Fp8Args {
   int a_e8m0, w_e8m0;
   int nbk, nbc;  // blocks along K and C
   uint16_t *out;  // bf16 [cap,C]; SwiGLU: h_save, or null
+  uint8_t *ys;    // down projection, 256-wide tiles: out is fp16 with scales [cap, ceil(C/kYCols)]
   // SwiGLU: C = 2I; a = silu(gate) up in e4m3 [cap,I] with e8m0 scales [cap, ceil(I/128)]
   uint8_t *aq;
   uint8_t *aq_scale;
