@@ -82,6 +82,15 @@ __device__ __forceinline__ u32x4 columns8(u32x2 a, u32x2 b) {
   }
   return v;
 }
+// maximum over the four lanes that share a token
+__device__ __forceinline__ uint32_t max4(uint32_t m) {
+  const auto h = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+  m = h[0] > h[1] ? h[0] : h[1];
+  const auto q = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+  return q[0] > q[1] ? q[0] : q[1];
+}
+constexpr uint32_t kInf = 0x7f800000u;
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 __device__ __forceinline__ u32x2 to_bf16(const f32x4 &v) {
   return u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
@@ -452,21 +461,23 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
     uint16_t *o = g.out + s * g.C;
     float by = 1.0f;
     if (!SWI && g.ys) {
+      // the largest of the bits of |y|; where that is no finite value's (rare), of the finite ones
       uint32_t m = 0;
+      auto largest = [&](auto bits) {
+        m = 0;
 #pragma unroll
-      for (int n = 0; n < TN; n++) {
-        const bool in = nt * BN + wn * (BN / WN) + n * 16 + fg * 4 < g.C;
+        for (int n = 0; n < TN; n++) {
+          if (nt * BN + wn * (BN / WN) + n * 16 >= g.C) continue;  // whole pieces, uniform
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const uint32_t b = finite_abs_bits(acc[n][t][i]);
-          m = in && b > m ? b : m;
+          for (int i = 0; i < 4; i++) {
+            const uint32_t b = bits(acc[n][t][i]);
+            m = b > m ? b : m;
+          }
         }
-      }
-#pragma unroll
-      for (int h = 16; h < 64; h <<= 1) {
-        const uint32_t u = (uint32_t)__shfl_xor((int)m, h, kWave);
-        m = m > u ? m : u;
-      }
+      };
+      largest(abs_bits);
+      if (ballot64(m >= kInf)) largest(finite_abs_bits);
+      m = max4(m);
       const uint32_t ex = y_exponent(m);
       by = __uint_as_float((268u - ex) << 23);
       const int c0 = nt * BN + wn * (BN / WN);
@@ -494,22 +505,30 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
       uint32_t m = 0;
 #pragma unroll
       for (int n = 0; n < TN; n++) {
-        const int c = nt * BN + wn * (BN / WN) + n * 16 + fg * 4;
-        const bool in = c < g.C;
+        const bool in = nt * BN + wn * (BN / WN) + n * 16 < g.C;  // whole pieces, uniform
         const f32x4 v = acc[n][t];
 #pragma unroll
         for (int p = 0; p < 2; p++) {
           const float a = silu_fast(v[2 * p]) * v[2 * p + 1];  // a few 2^-24, far below h's error
-          const uint32_t b = finite_abs_bits(a);
           av[n][t][p] = a;
-          m = in && b > m ? b : m;
+          const uint32_t b = in ? abs_bits(a) : 0;
+          m = b > m ? b : m;
         }
       }
+      if (ballot64(m >= kInf)) {  // rare: what is not finite becomes NaN and sets no scale
+        m = 0;
 #pragma unroll
-      for (int s = 16; s < 64; s <<= 1) {
-        const uint32_t u = (uint32_t)__shfl_xor((int)m, s, kWave);
-        m = m > u ? m : u;
+        for (int n = 0; n < TN; n++) {
+          const bool in = nt * BN + wn * (BN / WN) + n * 16 < g.C;
+#pragma unroll
+          for (int p = 0; p < 2; p++) {
+            const uint32_t b = abs_bits(av[n][t][p]);
+            if (b >= kInf) av[n][t][p] = __uint_as_float(0x7fc00000u);
+            m = in && b < kInf && b > m ? b : m;
+          }
+        }
       }
+      m = max4(m);
       if (fg == 0) s_max[wn][tok] = m;
     }
     __syncthreads();
@@ -524,19 +543,16 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
       const float inv = exponent_inverse(ex);
       // The lane's two bytes of each piece; the four lanes of a token then exchange them, so
       // that lane fg has the eight bytes of piece fg.
-      const uint32_t a01 = pack_e4m3(to_q(av[0][t][0], inv), to_q(av[0][t][1], inv),
-                                     to_q(av[1][t][0], inv), to_q(av[1][t][1], inv));
-      const uint32_t a23 = pack_e4m3(to_q(av[2][t][0], inv), to_q(av[2][t][1], inv),
-                                     to_q(av[3][t][0], inv), to_q(av[3][t][1], inv));
-      const bool up = fg & 2, odd = fg & 1;
-      const uint32_t mine = up ? a23 : a01;
-      const uint32_t his = (uint32_t)__shfl_xor((int)(up ? a01 : a23), 32, kWave);
-      const uint32_t w0 = up ? his : mine, w1 = up ? mine : his;  // of lanes fg & 1, 2 + fg & 1
-      const uint32_t keep = odd ? (w0 >> 16) | (w1 & 0xffff0000u) : (w0 & 0xffffu) | (w1 << 16);
-      const uint32_t give = odd ? (w0 & 0xffffu) | (w1 << 16) : (w0 >> 16) | (w1 & 0xffff0000u);
-      const uint32_t got = (uint32_t)__shfl_xor((int)give, 16, kWave);
-      const uint32_t ev = odd ? got : keep, od = odd ? keep : got;  // of even and odd lanes
-      const u32x2 q = {(ev & 0xffffu) | (od << 16), (ev >> 16) | (od & 0xffff0000u)};
+      uint32_t b[TN];
+#pragma unroll
+      for (int n = 0; n < TN; n++)
+        b[n] = pack_e4m3(av[n][t][0] * inv, av[n][t][1] * inv, 0.0f, 0.0f);
+      // a 4 x 4 exchange of 16 bits: rows of 32 lanes, then of 16
+      const auto h0 = __builtin_amdgcn_permlane32_swap(b[0], b[2], false, false);
+      const auto h1 = __builtin_amdgcn_permlane32_swap(b[1], b[3], false, false);
+      const auto q0 = __builtin_amdgcn_permlane16_swap(h0[0], h1[0], false, false);
+      const auto q1 = __builtin_amdgcn_permlane16_swap(h0[1], h1[1], false, false);
+      const u32x2 q = {q0[0] | (q0[1] << 16), q1[0] | (q1[1] << 16)};
       const int j = nt * kQB + wn * (BN / WN / 2) + fg * 8;
       if (even || (tok < rows && j < I))
         *(u32x2 *)(g.aq + (int64_t)(row0 + (tok < rows ? tok : 0)) * I + j) = q;
