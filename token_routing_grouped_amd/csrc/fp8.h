@@ -23,6 +23,12 @@ __device__ __forceinline__ uint32_t scale_exponent(uint32_t amax_bits) {
   return (uint32_t)(e > 1 ? e : 1);
 }
 __device__ __forceinline__ float exponent_value(uint32_t e) { return __uint_as_float(e << 23); }
+// a scale as it was passed in, any of its type's values: byte 0 is 2^-127, 255 NaN
+__device__ __forceinline__ float scale_value(const void *p, int e8m0, int64_t i) {
+  if (!e8m0) return ((const float *)p)[i];
+  const uint32_t b = ((const uint8_t *)p)[i];
+  return __uint_as_float(b - 1 < 254 ? b << 23 : b ? 0x7fc00000u : 0x400000u);
+}
 __device__ __forceinline__ float exponent_inverse(uint32_t e) {
   return __uint_as_float((254u - e) << 23);
 }

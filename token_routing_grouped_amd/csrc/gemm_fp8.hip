@@ -61,10 +61,6 @@ __device__ __forceinline__ uint32_t lds_address(const void *p) {
       (int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p);
 }
 
-__device__ __forceinline__ float scale_value(const void *p, int e8m0, int64_t i) {
-  return e8m0 ? exponent_value(((const uint8_t *)p)[i]) : ((const float *)p)[i];
-}
-
 constexpr int kKC = 8;  // blocks of K whose scales LDS holds at a time (two such sets)
 
 // Four lanes that share a token (16 apart) hold four consecutive bf16 columns each of pieces

@@ -32,10 +32,6 @@ __device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
   return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-__device__ __forceinline__ float scale_value(const void *p, int e8m0, int64_t i) {
-  return e8m0 ? exponent_value(((const uint8_t *)p)[i]) : ((const float *)p)[i];
-}
-
 constexpr int kSB = 48;  // blocks of K whose scales LDS holds at a time
 
 // TT: 16-row pieces of a tile; NW: waves, TN 16-column pieces each; U: blocks in flight (of
