@@ -203,7 +203,12 @@ moe_status moe_expert_backward(const moe_metadata *meta, const int32_t *topk_idx
  * max|v| <= 448 s over the block's finite values, at least 2^-126. Quotients v/s are
  * then exact, and each value is rounded once: to nearest, ties to even. A value that is
  * not finite becomes NaN (and nothing else in its block changes).
- * e4m3 rows and weights need lengths that are multiples of 16 in the products. */
+ * e4m3 rows and weights need lengths that are multiples of 16 in the products.
+ *
+ * Addresses. Tensors and workspaces of these calls start at multiples of 16 bytes (what
+ * moe_quantize_rows and the norm write as q: of 8), fp32 scales and rstd of 4, e8m0 scales
+ * anywhere; MOE_EINVAL otherwise. Apart from the outputs that are said to be allowed in the
+ * place of an input, outputs and inputs do not overlap. */
 typedef enum { MOE_SCALE_FP32 = 0, MOE_SCALE_E8M0 = 1 } moe_scale_type;
 enum { MOE_QBLOCK = 128 };
 

@@ -100,7 +100,9 @@ def test_expert_forward_refusals():
     f, ws = L().moe_expert_forward_fp8, L().moe_expert_forward_fp8_workspace
     need = ws(meta(), 64, 32)
     assert need == 256 + 256 + 8 * 64 * 2 + 8 * 32 * 4
-    assert ws(meta(cap=61), 64, 32) == 2048 + 256 + 61 * 64 * 2 + 128 + 256
+    assert ws(meta(cap=61), 64, 32) == 2048 + 256 + 7936 + 7936  # few tiles of 32 rows
+    n = 1 << 16  # neither few rows per expert nor few tiles
+    assert ws(meta(cap=n), 64, 32) == n * 32 + n + n * 64 * 2 + n
 
     def call(m=None, x=A, xs=A, tx=0, u=A, us=A, d=A, ds=A, tw=0, H=64, I=32, lay=0, out=A, wk=A, nb=need):
         return f(meta() if m is None else m, x, xs, tx, u, us, d, ds, tw, H, I, lay, None, out, wk, nb, None)
@@ -113,6 +115,30 @@ def test_expert_forward_refusals():
         assert call(**{k: None}) == EINVAL
     assert call(nb=need - 1) == ENOSPC and call(wk=None) == ENOSPC
     assert call(m=meta(N=0), x=None, out=None) == OK
+
+
+def test_refusals_of_addresses():
+    """16 bytes for what is read and written in pieces of 16, 8 for q of rows, 4 for fp32 scales
+    and rstd; e8m0 scales anywhere."""
+    l = L()
+    B, R, Z = A + 8, A + 4, A + 2
+    assert l.moe_quantize_rows(B, 1, 64, 0, A, A, 0, None) == EINVAL
+    assert l.moe_quantize_rows(A, 1, 64, 0, R, A, 0, None) == EINVAL
+    assert l.moe_quantize_rows(A, 1, 64, 0, A, Z, 0, None) == EINVAL
+    for w, q, s in ((B, A, A), (A, B, A), (A, A, Z)):
+        assert l.moe_quantize_weights(w, 1, 64, 64, 0, q, s, 0, None) == EINVAL
+    ok = [A, A, A, 1e-6, 1, 64, 0, A, A, A, A, 0, A, None]
+    for i, v in ((0, B), (1, B), (2, B), (7, B), (8, B), (9, R), (10, Z), (12, Z)):
+        assert l.moe_rmsnorm_forward(*ok[:i], v, *ok[i + 1:]) == EINVAL
+    ok = [A, A, A, A, A, 1, 64, 0, A, A, A, 1 << 20, None]
+    for i, v in ((0, B), (1, B), (2, B), (3, Z), (4, B), (8, B), (9, B), (10, B)):
+        assert l.moe_rmsnorm_backward(*ok[:i], v, *ok[i + 1:]) == EINVAL
+    ok = [meta(), A, A, 0, A, A, 0, 64, 64, 1, A, None]
+    for i, v in ((1, B), (2, Z), (4, B), (5, Z), (10, B)):
+        assert l.moe_grouped_gemm_fp8(*ok[:i], v, *ok[i + 1:]) == EINVAL
+    ok = [meta(), A, A, 0, A, A, A, A, 0, 64, 32, 0, A, A, A, 1 << 20, None]
+    for i, v in ((1, B), (2, Z), (4, B), (5, Z), (6, B), (7, Z), (12, B), (13, B), (14, B)):
+        assert l.moe_expert_forward_fp8(*ok[:i], v, *ok[i + 1:]) == EINVAL
 
 
 def test_binding_refuses_host_tensors():

@@ -262,6 +262,15 @@ SHAPES = [  # N, K, C, E, topk, p_invalid
     (700, 2048, 320, 2, 2, 0.0),
     (64, 4112, 128, 40, 4, 0.5),
     (17, 256, 1040, 200, 8, 0.0),
+    (20, 6416, 144, 3, 2, 0.0),    # more blocks along K than the kernel for few rows keeps scales of
+    (900, 400, 592, 5, 2, 0.1),    # from here on 256 x 256 tiles: neither few rows nor few tiles
+    (1100, 1040, 1040, 3, 2, 0.0),
+    (2100, 16, 512, 1, 1, 0.0),
+    (2100, 144, 528, 2, 1, 0.1),
+    (5200, 128, 2048, 3, 2, 0.0),  # more tiles than CUs: one block of K, two, three; odd columns
+    (5200, 256, 2064, 3, 2, 0.0),
+    (5200, 384, 2048, 3, 2, 0.1),
+    (1300, 128, 1024, 40, 1, 0.0),
 ]
 
 
@@ -289,7 +298,7 @@ def test_grouped_product(shape, kinds):
 
 
 @pytest.mark.parametrize("kinds", ["e8m0 e8m0", "fp32 fp32"])
-@pytest.mark.parametrize("N,K,C,E", [(20, 16, 32, 1), (150, 528, 144, 3), (260, 2176, 272, 2)])
+@pytest.mark.parametrize("N,K,C,E", [(20, 16, 32, 1), (150, 528, 144, 3), (260, 2176, 272, 2), (2100, 656, 528, 3)])
 def test_grouped_product_of_narrow_values(N, K, C, E, kinds):
     """Values of four powers of two: products of an aligned group span six, with six bits each
     below their own power, so nothing lies 2^13 below the largest; only fp32 roundings remain."""
@@ -309,11 +318,12 @@ def test_grouped_product_of_narrow_values(N, K, C, E, kinds):
         assert np.all(np.abs(host(out)[lo:hi] - ref) <= (mag * (K + 16) * fp8.U32 + np.abs(ref) * fp8.HALF["bf16"]) * (1 + 1e-2))
 
 
-@pytest.mark.parametrize("N", [6, 80])
+@pytest.mark.parametrize("N", [6, 80, 8300])
 def test_grouped_product_alignment_of_eight(N):
     """The matrix cores' rule that the bounds use: next to a product of 2^16 in the same eight
     values of K one of 2^3 counts and those of 2^2 are cut off, one by one; in another eight
-    they count in full. With few rows (N = 6) the products are widened, and all count."""
+    they count in full. With few rows or few tiles (N below 8161: 255 tiles of 32 rows) the
+    products are widened, and all count."""
     import torch
     c = Case(N, 128, 1, 1, seed=0, p_invalid=0.0)
     a, w = np.zeros((N, 128), np.uint8), np.zeros((1, 16, 128), np.uint8)
@@ -328,34 +338,73 @@ def test_grouped_product_alignment_of_eight(N):
     moe().moe_grouped_gemm_fp8(c.meta, t(a), s, t(w), s[:1].view(1, 1, 1), out)
     want = np.zeros(N)
     want[1], want[4], want[5] = 8, 2.0 ** -4, 2.0 ** -5
-    if N == 6:
+    if N < 8161:
         want[2], want[3] = 4, 28
     assert np.array_equal(host(out), np.repeat(want[c.rows][:, None], 16, 1))
 
 
-def test_grouped_product_leaves_rows_behind_the_last():
+@pytest.mark.parametrize("N,C", [(50, 144), (1500, 512), (1500, 528)])
+def test_grouped_product_leaves_rows_behind_the_last(N, C):
     import torch
-    c = Case(50, 160, 6, 2, seed=3, capacity=100)
-    assert c.P < 100
-    a, sa, va = c.operand((50, 160), "e8m0")
-    w, sw, vw = c.operand((6, 144, 160), "e8m0")
-    out = torch.full((100, 144), -5.0, dtype=torch.bfloat16, device="cuda")
+    c = Case(N, 160, 6, 2, seed=3, capacity=2 * N)
+    assert c.P < 2 * N
+    a, sa, va = c.operand((N, 160), "e8m0")
+    w, sw, vw = c.operand((6, C, 160), "e8m0")
+    out = torch.full((2 * N, C), -5.0, dtype=torch.bfloat16, device="cuda")
     moe().moe_grouped_gemm_fp8(c.meta, a, sa, w, sw, out)
     ref, err = fp8.grouped(*va, *vw, c.off, c.rows)
     assert np.all(np.abs(host(out)[:c.P] - ref) <= (err + np.abs(ref) * fp8.HALF["bf16"]) * (1 + 1e-2))
     assert torch.all(out[c.P:] == -5.0)
     # more pairs than the capacity: nothing is written
-    c2 = Case(50, 160, 6, 2, seed=3, capacity=c.P - 1)
-    out2 = torch.full((c.P - 1, 144), -5.0, dtype=torch.bfloat16, device="cuda")
+    c2 = Case(N, 160, 6, 2, seed=3, capacity=c.P - 1)
+    out2 = torch.full((c.P - 1, C), -5.0, dtype=torch.bfloat16, device="cuda")
     moe().moe_grouped_gemm_fp8(c2.meta, a, sa, w, sw, out2)
     assert torch.all(out2 == -5.0)
     assert int(c2.meta.status.item()) & moe().MOE_DEV_OVER_CAPACITY
 
 
-def test_grouped_product_nan_stays_in_its_row_and_column():
+@pytest.mark.parametrize("kinds", ["e8m0 e8m0", "fp32 e8m0", "e8m0 fp32"])
+@pytest.mark.parametrize("N", [10, 70, 4300])
+def test_grouped_product_of_extreme_scales(N, kinds):
+    """The smallest and the largest scales of each type next to others that bring the products
+    back, and an e8m0 NaN."""
     import torch
-    c = Case(70, 272, 3, 1, seed=5, p_invalid=0.0)
-    a, sa, va = c.operand((70, 272), "e8m0")
+    ka, kw = kinds.split()
+    c = Case(N, 272, 3, 1, seed=7, p_invalid=0.0)
+    a, sa, va = c.operand((N, 272), ka)
+    w, sw, vw = c.operand((3, 160, 272), kw, 2.0 ** 40)
+    ea = np.full((N, 3), -126 if ka == "fp32" else -127)
+    ea[1::3] = -100
+    s = np.exp2(ea.astype(np.float64))
+    t = np.exp2(np.floor(np.log2(vw[1][:, ::128, ::128])))
+    t[2] = 2.0 ** 127  # expert 2: the largest
+
+    def put(s, kind):
+        if kind == "fp32":
+            return torch.from_numpy(s.astype(np.float32)).cuda()
+        return torch.from_numpy((np.log2(s) + 127).astype(np.uint8)).cuda().view(torch.float8_e8m0fnu)
+
+    oa, ow = fp8.spread(s, 272), fp8.spread2(t, 160, 272)
+    ref, err = fp8.grouped(va[0] / va[1] * oa, oa, vw[0] / vw[1] * ow, ow, c.off, c.rows)
+    sa, sw = put(s, ka), put(t, kw)
+    out = torch.empty(c.cap, 160, dtype=torch.bfloat16, device="cuda")
+    moe().moe_grouped_gemm_fp8(c.meta, a, sa, w, sw, out)
+    assert np.all(np.abs(host(out) - ref) <= (err + np.abs(ref) * fp8.HALF["bf16"]) * (1 + 1e-2))
+    if ka == "e8m0":
+        sa.view(torch.uint8)[c.rows[3], 1] = 255
+        out2 = torch.empty_like(out)
+        moe().moe_grouped_gemm_fp8(c.meta, a, sa, w, sw, out2)
+        assert torch.isnan(out2[3]).all()
+        keep = [i for i in range(c.cap) if i != 3]
+        assert torch.equal(out2[keep], out[keep])
+
+
+@pytest.mark.parametrize("kind", ["e8m0", "fp32"])
+@pytest.mark.parametrize("N", [10, 70, 4300])
+def test_grouped_product_nan_stays_in_its_row_and_column(N, kind):
+    import torch
+    c = Case(N, 272, 3, 1, seed=5, p_invalid=0.0)
+    a, sa, va = c.operand((N, 272), kind)
     w, sw, vw = c.operand((3, 160, 272), "e8m0")
     out = torch.empty(c.cap, 160, dtype=torch.bfloat16, device="cuda")
     moe().moe_grouped_gemm_fp8(c.meta, a, sa, w, sw, out)
@@ -405,6 +454,11 @@ EXPERTS = [  # N, H, I, E, topk, p_invalid
     (150, 256, 64, 3, 2, 0.1),
     (400, 400, 336, 5, 2, 0.1),
     (90, 2064, 528, 2, 2, 0.0),
+    (1500, 64, 592, 2, 1, 0.0),    # 256 x 256 tiles for the up projection
+    (1500, 1040, 48, 2, 1, 0.1),   # for the down projection
+    (2000, 272, 144, 3, 2, 0.1),   # from here on for both
+    (2500, 384, 256, 4, 2, 0.0),
+    (6400, 256, 1024, 3, 2, 0.0),  # more tiles than CUs
 ]
 
 
@@ -444,13 +498,264 @@ def test_expert_forward_rows_without_slots_and_over_capacity():
     assert torch.all(out == 0) and torch.isnan(h).all()
 
 
+@pytest.mark.parametrize("H,I", [(128, 48), (1152, 640)])
 @pytest.mark.parametrize("sizes", [(0, 1, 127, 128, 129, 255, 256, 257)])
-def test_expert_forward_segment_sizes(sizes):
+def test_expert_forward_segment_sizes(sizes, H, I):
     """Segments of every length around the tiles' edges, empty ones among them."""
     idx = np.repeat(np.arange(len(sizes)), sizes).astype(np.int32)
     idx = np.random.default_rng(0).permutation(idx).reshape(-1, 1)
-    c = Case(len(idx), 128, len(sizes), 1, seed=2, idx=idx)
+    c = Case(len(idx), H, len(sizes), 1, seed=2, idx=idx)
     for kinds in ("e8m0 e8m0", "fp32 fp32"):
-        _, vals, out, _ = run_experts(c, 128, 48, *kinds.split(), 0)
+        _, vals, out, _ = run_experts(c, H, I, *kinds.split(), 0)
         ro, bo, _, _ = expected(c, vals, 0)
         assert np.all(np.abs(host(out) - ro) <= bo * (1 + 1e-2))
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("N,H,I", [(12, 256, 80), (150, 256, 80), (1500, 1040, 592)])
+def test_expert_forward_nan_stays_in_its_token(N, H, I, layout):
+    import torch
+    c = Case(N, H, 3, 2, seed=9, p_invalid=0.1)
+    ops, _, out, h = run_experts(c, H, I, "e8m0", "e8m0", layout)
+    x2, sx2 = ops[0].clone(), ops[1].clone()
+    x2.view(torch.uint8)[3, 7], sx2.view(torch.uint8)[5, 1] = 0x7f, 0xff
+    out2, h2 = torch.empty_like(out), torch.full_like(h, float("nan"))
+    moe().moe_expert_forward_fp8(c.meta, x2, sx2, *ops[2:], out2, h_save=h2, layout=layout)
+    bad = np.zeros(N, bool)
+    bad[[t for t in (3, 5) if (c.idx[t] >= 0).any()]] = True
+    assert bad.any()
+    assert np.array_equal(np.isnan(host(out2)), np.repeat(bad[:, None], H, 1))
+    keep = torch.from_numpy(~bad).cuda()
+    assert torch.equal(out2[keep], out[keep])
+    assert np.array_equal(np.isnan(host(h2)[:c.P]).all(1), bad[c.rows])
+
+
+def test_expert_forward_huge_and_tiny_values():
+    """h and y from 2^-60 to 2^60 between rows of one batch, as far as fp32 scales reach
+    (no overflow of the 16-bit y between the products), for few rows and for tiles."""
+    import torch
+    for N, H, I in ((40, 256, 80), (1500, 1040, 592)):
+        c = Case(N, H, 2, 2, seed=4, p_invalid=0.0)
+        m = moe()
+        x, sx, _ = c.operand((N, H), "fp32")
+        u, su, vu = c.operand((2, 2 * I, H), "fp32", 2.0 ** -7)
+        d, sd, vd = c.operand((2, H, I), "fp32", 2.0 ** -7)
+        sx = sx * torch.exp2(torch.arange(N, device="cuda") % 31 * 2.0 - 30)[:, None]  # silu(g) u: squared
+        over = fp8.spread(host(sx), H)
+        vx = (fp8.e4m3_decode(x.view(torch.uint8).cpu().numpy()) * over, over)
+        out = torch.empty(N, H, dtype=torch.bfloat16, device="cuda")
+        m.moe_expert_forward_fp8(c.meta, x, sx, u, su, d, sd, out)
+        ro, bo, _, _ = expected(c, (vx, vu, vd), 0)
+        assert np.all(np.abs(host(out) - ro) <= bo * (1 + 1e-2))
+
+
+def test_expert_forward_duplicates_and_most_experts():
+    idx = np.random.default_rng(0).integers(0, 1024, (300, 3)).astype(np.int32)
+    idx[:, 2] = idx[:, 0]
+    idx[7] = -1
+    for H, I in ((144, 48), (64, 16)):
+        c = Case(300, H, 1024, 3, seed=6, idx=idx)
+        _, vals, out, _ = run_experts(c, H, I, "e8m0", "fp32", 1)
+        ro, bo, _, _ = expected(c, vals, 1)
+        assert np.all(np.abs(host(out) - ro) <= bo * (1 + 1e-2))
+
+
+@pytest.mark.parametrize("N,H,I", [(9, 144, 48), (1500, 64, 592), (1500, 1040, 48), (2000, 272, 144)])
+def test_expert_forward_stays_in_its_workspace(N, H, I):
+    import torch
+    c = Case(N, H, 2, 1, seed=8, p_invalid=0.0)
+    ops, _, out, _ = run_experts(c, H, I, "e8m0", "e8m0", 0)
+    n = moe().moe_expert_forward_fp8_workspace(c.meta, H, I)
+    ws = torch.full((n + 4096,), 0xff, dtype=torch.uint8, device="cuda")
+    out2 = torch.empty_like(out)
+    moe().moe_expert_forward_fp8(c.meta, *ops, out2, workspace=ws[:n])
+    assert torch.equal(out2, out) and torch.all(ws[n:] == 0xff)
+
+
+# ---- offsets past 32 bits ---------------------------------------------------------------------
+
+
+def big_operand(shape, seed):
+    """Codes of magnitudes in [0.5, 1), made on the device, with e8m0 scales of 2^0 and 2^1."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q = torch.randint(0, 256, shape, dtype=torch.uint8, device="cuda", generator=g)
+    q.bitwise_and_(0x87).bitwise_or_(0x30)
+    ss = (shape[0], cd(shape[1])) if len(shape) == 2 else (shape[0], cd(shape[1]), cd(shape[2]))
+    s = torch.randint(127, 129, ss, dtype=torch.uint8, device="cuda", generator=g)
+    return q.view(torch.float8_e4m3fn), s.view(torch.float8_e8m0fnu)
+
+
+def values(q, s):
+    """Values and scales over them of rows q with their rows of scales s."""
+    over = fp8.spread(host(s), q.shape[1])
+    return host(q) * over, over
+
+
+@pytest.mark.parametrize("N,K,C,E", [(270000, 16384, 32, 1), (5, 16400, 262160, 1), (40, 16400, 262160, 1),
+                                     (1500, 16384, 4096, 70), (70, 16384, 4096, 70), (300000, 256, 8192, 2)])
+def test_grouped_product_past_32_bits(N, K, C, E):
+    """Rows, one expert's weights, all experts' weights or the output past 4 GiB (and 2^31
+    values): a sample of rows, first and last ones among them, at a sample of columns."""
+    import torch
+    say("past 32 bits", N, K, C, E)
+    c = Case(N, K, E, 1, seed=N, p_invalid=0.0)
+    (a, sa), (w, sw) = big_operand((N, K), 1), big_operand((E, C, K), 2)
+    out = torch.empty(c.cap, C, dtype=torch.bfloat16, device="cuda")
+    moe().moe_grouped_gemm_fp8(c.meta, a, sa, w, sw, out)
+    at = np.unique(np.r_[0, 1, c.P // 2, c.P - 2, c.P - 1, np.random.default_rng(0).integers(0, c.P, 20)].clip(0))
+    col = np.unique(np.r_[0, 17, C // 2, C - 1, np.random.default_rng(1).integers(0, C, 12)])
+    tcol = torch.from_numpy(col).cuda()
+    rows = torch.from_numpy(c.rows[at].astype(np.int64)).cuda()
+    va, oa = values(a.view(torch.uint8)[rows].view(a.dtype), sa.view(torch.uint8)[rows].view(sa.dtype))
+    for e in np.unique(np.searchsorted(c.off, at, "right") - 1):
+        mine = np.searchsorted(c.off, at, "right") - 1 == e
+        vw, ow = values(w[int(e)].view(torch.uint8)[tcol].view(w.dtype), sw[int(e)].view(torch.uint8)[tcol // 128].view(sw.dtype))
+        n = int(mine.sum())
+        ref, err = fp8.grouped(va[mine], oa[mine], vw[None], ow[None], np.array([0, n]), np.arange(n))
+        got = host(out[torch.from_numpy(at[mine]).cuda()][:, tcol])
+        assert np.all(np.abs(got - ref) <= (err + np.abs(ref) * fp8.HALF["bf16"]) * (1 + 1e-2))
+
+
+def test_expert_forward_past_32_bits():
+    """h and y past 4 GiB: the tokens' results do not depend on how many others there are,
+    so a sample of the tokens is checked against a call of their own."""
+    import torch
+    N, H, I, E = 140000, 8192, 4096, 2
+    idx = np.tile(np.int32([0, 1]), (N, 1))
+    c = Case(N, H, E, 2, seed=1, idx=idx)
+    (x, sx), (u, su), (d, sd) = big_operand((N, H), 1), big_operand((E, 2 * I, H), 2), big_operand((E, H, I), 3)
+    out = torch.empty(N, H, dtype=torch.bfloat16, device="cuda")
+    h = torch.empty(2 * N, 2 * I, dtype=torch.bfloat16, device="cuda")
+    moe().moe_expert_forward_fp8(c.meta, x, sx, u, su, d, sd, out, h_save=h)
+    pick = torch.from_numpy(np.r_[0:300, N - 300:N, np.random.default_rng(0).integers(0, N, 1000)]).cuda()
+    k = len(pick)
+    c2 = Case(k, H, E, 2, seed=1, idx=idx[:k])
+    c2.d_wt.copy_(c.d_wt[pick])
+    moe().moe_build_metadata(c2.d_idx, c2.d_wt, c2.meta)
+    x2, sx2 = (v.view(torch.uint8)[pick].view(v.dtype) for v in (x, sx))
+    out2 = torch.empty(k, H, dtype=torch.bfloat16, device="cuda")
+    h2 = torch.empty(2 * k, 2 * I, dtype=torch.bfloat16, device="cuda")
+    moe().moe_expert_forward_fp8(c2.meta, x2, sx2, u, su, d, sd, out2, h_save=h2)
+    assert torch.equal(out[pick], out2)
+    assert torch.equal(h[pick], h2[:k]) and torch.equal(h[pick + N], h2[k:])
+    # and these against the formula, at a few tokens
+    few = torch.arange(0, k, 211, device="cuda")
+    n = len(few)
+    vu = [np.stack(z) for z in zip(*(big_values(u[e], su[e]) for e in range(E)))]
+    vd = [np.stack(z) for z in zip(*(big_values(d[e], sd[e]) for e in range(E)))]
+    vx = values(x2.view(torch.uint8)[few].view(x.dtype), sx2.view(torch.uint8)[few].view(sx.dtype))
+    m = oracle.build_metadata(idx[:n], host(c2.d_wt[few]).astype(np.float32), E)
+    ro, bo, _, _ = fp8.experts(*vx, *vu, *vd, m["expert_frequency_offset"], m["x_gather_idx"],
+                               host(c2.d_wt[few]).reshape(-1)[m["s_scatter_idx"]], n)
+    assert np.all(np.abs(host(out2[few]) - ro) <= bo * (1 + 1e-2))
+
+
+def big_values(q, s):
+    over = fp8.spread2(host(s)[None], q.shape[0], q.shape[1])[0]
+    return host(q) * over, over
+
+
+def test_row_operators_past_32_bits():
+    """Rows past 4 GiB give what they give by themselves; dweight against a sum in 64 bits."""
+    import torch
+    N, H = 300000, 8192
+    m, g = moe(), torch.Generator(device="cuda").manual_seed(0)
+    x = torch.randn(N, H, dtype=torch.bfloat16, device="cuda", generator=g)
+    w = torch.randn(H, dtype=torch.bfloat16, device="cuda", generator=g)
+    pick = torch.cat([torch.arange(40), torch.arange(N - 40, N), torch.randint(0, N, (100,))]).cuda()
+
+    def rows(x, q, s, y=None, rstd=None):
+        m.moe_quantize_rows(x, q, s) if y is None else m.moe_rmsnorm_forward(x, w, y=y, q=q, scale=s, rstd=rstd)
+
+    def outputs(n):
+        return (q_tensor((n, H)), scale_tensor((n, cd(H)), "e8m0"), torch.empty(n, H, dtype=x.dtype, device="cuda"),
+                torch.empty(n, device="cuda"))
+
+    full, some = outputs(N), outputs(len(pick))
+    for k in (2, 4):
+        rows(x, *full[:k])
+        rows(x[pick], *some[:k])
+        for f, s in zip(full[:k], some[:k]):
+            b = (lambda t: t.view(torch.uint8)) if f.element_size() == 1 else (lambda t: t)
+            assert torch.equal(b(f)[pick], b(s))
+    dy, rstd = full[2], full[3]
+    dx, dw, dx2, dw2 = torch.empty_like(x), torch.empty_like(w), torch.empty_like(x[pick]), torch.empty_like(w)
+    m.moe_rmsnorm_backward(dy, x, w, rstd, dx, dw)
+    m.moe_rmsnorm_backward(dy[pick], x[pick], w, rstd[pick], dx2, dw2)
+    assert torch.equal(dx[pick], dx2)
+    ref, mag = torch.zeros(H, dtype=torch.float64, device="cuda"), torch.zeros(H, dtype=torch.float64, device="cuda")
+    for i in range(0, N, 20000):
+        v = dy[i:i + 20000].double() * x[i:i + 20000].double() * rstd[i:i + 20000, None].double()
+        ref += v.sum(0)
+        mag += v.abs().sum(0)
+    tol = mag * ((N / 64 + 80) * fp8.U32) + ref.abs() * fp8.HALF["bf16"] * (1 + 1e-3)
+    assert torch.all((dw.double() - ref).abs() <= tol)
+
+
+def test_quantize_weights_past_32_bits():
+    import torch
+    E, L = 34, 8192
+    w = torch.randn(E, L, L, dtype=torch.bfloat16, device="cuda", generator=torch.Generator(device="cuda").manual_seed(0))
+    q, s = q_tensor((E, L, L)), scale_tensor((E, 64, 64), "e8m0")
+    moe().moe_quantize_weights(w, q, s)
+    for e in (0, E - 1):
+        q2, s2 = q_tensor((1, L, L)), scale_tensor((1, 64, 64), "e8m0")
+        moe().moe_quantize_weights(w[e:e + 1], q2, s2)
+        assert torch.equal(q[e].view(torch.uint8), q2[0].view(torch.uint8))
+        assert torch.equal(s[e].view(torch.uint8), s2[0].view(torch.uint8))
+
+
+# ---- refusals of the binding --------------------------------------------------------------------
+
+
+def test_binding_refusals():
+    import torch
+    m = moe()
+    c = Case(6, 64, 2, 2, seed=1)
+    ops, _, out, h = run_experts(c, 64, 32, "e8m0", "e8m0", 0)
+    x, sx, u, su, d, sd = ops
+    f = lambda **k: m.moe_expert_forward_fp8(c.meta, *[k.get(n, v) for n, v in zip(("x", "sx", "u", "su", "d", "sd"), ops)],
+                                             k.get("out", out), h_save=k.get("h"), workspace=k.get("ws"),
+                                             layout=k.get("layout", 0))
+    for n in ("x", "sx", "u", "su", "d", "sd", "out"):
+        with pytest.raises(TypeError, match="device tensor"):
+            f(**{n: dict(zip(("x", "sx", "u", "su", "d", "sd", "out"), ops + (out,)))[n].cpu()})
+    with pytest.raises(TypeError, match="float8_e4m3fn"):
+        f(x=x.view(torch.uint8))
+    with pytest.raises(TypeError, match="float8_e8m0fnu"):
+        f(sx=sx.view(torch.uint8))
+    with pytest.raises(TypeError, match="w_down_scale"):
+        f(sd=sd.float())  # both weights' scales alike
+    with pytest.raises(ValueError, match="shape"):
+        f(sx=sx[:, :0])
+    with pytest.raises(ValueError, match="shape"):
+        f(u=u[:, :32])
+    with pytest.raises(ValueError, match="contiguous"):
+        f(x=x.view(torch.uint8).t().contiguous().t().view(x.dtype))
+    with pytest.raises(m.MoeError):
+        f(ws=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="workspace"):
+        f(ws=torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(m.MoeError):
+        f(layout=2)
+    off = torch.empty(6 * 64 + 8, dtype=torch.uint8, device="cuda")[8:].view(6, 64).view(x.dtype)
+    with pytest.raises(m.MoeError, match="invalid"):
+        f(x=off)  # not at a multiple of 16 bytes
+    out2 = torch.empty_like(out)
+    f(out=out2)
+    assert torch.equal(out2, out)
+    y = torch.empty(6, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(m.MoeError):
+        m.moe_rmsnorm_forward(y, w)  # no output
+    with pytest.raises(m.MoeError):
+        m.moe_rmsnorm_forward(y, w, residual=y, y=torch.empty_like(y))  # nowhere for the sum
+    with pytest.raises(TypeError, match="weight"):
+        m.moe_rmsnorm_forward(y, w.float(), y=torch.empty_like(y))
+    with pytest.raises(m.MoeError):
+        m.moe_rmsnorm_forward(y, w, eps=float("nan"), y=torch.empty_like(y))
+    with pytest.raises(ValueError, match="shape"):
+        m.moe_grouped_gemm_fp8(c.meta, x, sx, u, su, torch.empty(c.cap - 1, 64, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError, match="dimensions"):
+        m.moe_quantize_weights(y, y, y)

@@ -366,19 +366,24 @@ def _first(t, name: str, dims: int):
 
 class _Device:
     """Runs a call with `device` current (switched only when another one is); an explicit
-    stream must be on it. Gives the stream's handle."""
+    stream must be on it. Gives the stream's handle (the current stream's without building a
+    Stream object, which takes longer than the launch)."""
+
+    __slots__ = ("handle", "other")
 
     def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
+        if stream is None:
+            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
+        elif stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the call on {device}")
-        self.stream = stream
+        else:
+            self.handle = stream.cuda_stream
         self.other = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
 
     def __enter__(self):
         if self.other is not None:
             self.other.__enter__()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream()
-        return s.cuda_stream
+        return self.handle
 
     def __exit__(self, *exc):
         if self.other is not None:

@@ -12,27 +12,17 @@ inline bool scale_ok(moe_scale_type s) { return s == MOE_SCALE_FP32 || s == MOE_
 inline bool row_ok(int32_t H) { return H > 0 && H % 8 == 0 && H <= (1 << 20); }
 // sides of an 8-bit product: whole 16-byte chunks
 inline bool side_ok(int32_t L, int32_t most) { return L > 0 && L % 16 == 0 && L <= most; }
+// Addresses that the kernels read and write 16 (q: 8) bytes at a time, and fp32 scales. (Null
+// passes: whether a tensor may be missing is checked where it is taken.)
+template <typename... P>
+inline bool at16(const P *...p) {
+  return ((((uintptr_t)p | ...) & 15) == 0);
+}
+inline bool scale_at(const void *p, moe_scale_type t) {
+  return t == MOE_SCALE_E8M0 || ((uintptr_t)p & 3) == 0;
+}
 inline int32_t blocks(int32_t L) { return (L + MOE_QBLOCK - 1) / MOE_QBLOCK; }
 inline moe_status status_of(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
-
-struct Fp8Ws {
-  size_t aq, as, y, ys, af, total;
-};
-Fp8Ws fp8_layout(const moe_metadata *m, int32_t H, int32_t I) {
-  const size_t cap = (size_t)m->capacity;
-  Fp8Ws w;
-  w.aq = 0;
-  w.as = w.aq + align_up(cap * (size_t)I);
-  w.y = w.as + align_up(cap * (size_t)blocks(I));
-  Fp8Args g = {};
-  g.E = m->E;
-  g.cap = m->capacity;
-  const bool skinny = fp8_skinny(g);  // a in fp32 first; else scales of y
-  w.ys = w.y + align_up(cap * (size_t)H * 2);
-  w.af = w.ys + (skinny ? 0 : align_up(cap * (size_t)((H + kYCols - 1) / kYCols)));
-  w.total = w.af + (skinny ? align_up(cap * (size_t)I * sizeof(float)) : 0);
-  return w;
-}
 
 Fp8Args fp8_args(const moe_metadata *m, int32_t K, int32_t C) {
   Fp8Args g = {};
@@ -46,6 +36,23 @@ Fp8Args fp8_args(const moe_metadata *m, int32_t K, int32_t C) {
   return g;
 }
 
+struct Fp8Ws {
+  size_t aq, as, y, ys, af, total;
+};
+Fp8Ws fp8_layout(const moe_metadata *m, int32_t H, int32_t I) {
+  const size_t cap = (size_t)m->capacity;
+  Fp8Ws w;
+  w.aq = 0;
+  w.as = w.aq + align_up(cap * (size_t)I);
+  w.y = w.as + align_up(cap * (size_t)blocks(I));
+  // kernel for few rows: up, a in fp32 first; down, no scales of y
+  const bool up = fp8_skinny(fp8_args(m, H, 2 * I)), down = fp8_skinny(fp8_args(m, I, H));
+  w.ys = w.y + align_up(cap * (size_t)H * 2);
+  w.af = w.ys + (down ? 0 : align_up(cap * (size_t)((H + kYCols - 1) / kYCols)));
+  w.total = w.af + (up ? align_up(cap * (size_t)I * sizeof(float)) : 0);
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -55,6 +62,7 @@ moe_status moe_quantize_rows(const void *x, int32_t N, int32_t H, moe_dtype dt, 
   if (N < 0) return MOE_EINVAL;
   if (!dtype_ok(dt) || !scale_ok(scale_type) || !row_ok(H)) return MOE_EUNSUPPORTED;
   if (N > 0 && (!x || !q || !scale)) return MOE_EINVAL;
+  if (!at16(x) || (uintptr_t)q % 8 || !scale_at(scale, scale_type)) return MOE_EINVAL;
   // 16 lanes per block of 128, fewer than 2^32 in a launch
   if ((int64_t)N * blocks(H) >= (1 << 28) - 16) return MOE_EUNSUPPORTED;
   if (N == 0) return MOE_OK;
@@ -70,7 +78,7 @@ moe_status moe_quantize_weights(const void *w, int32_t E, int32_t K, int32_t C, 
   if (E < 1 || E > MOE_MAX_EXPERTS) return MOE_EINVAL;
   if (!dtype_ok(dt) || !scale_ok(scale_type)) return MOE_EUNSUPPORTED;
   if (!side_ok(K, 1 << 20) || !side_ok(C, 1 << 21)) return MOE_EUNSUPPORTED;
-  if (!w || !q || !scale) return MOE_EINVAL;
+  if (!w || !q || !scale || !at16(w, q) || !scale_at(scale, scale_type)) return MOE_EINVAL;
   // a workgroup of 256 lanes per block, fewer than 2^32 lanes in a launch
   if ((int64_t)E * blocks(K) * blocks(C) >= 1 << 24) return MOE_EUNSUPPORTED;
   hipStream_t st = (hipStream_t)stream;
@@ -90,6 +98,9 @@ moe_status moe_rmsnorm_forward(const void *x, const void *residual, const void *
     if (!x || !weight || (!y && !q) || (!q != !scale) || (!residual != !residual_out))
       return MOE_EINVAL;
   }
+  if (!at16(x, residual, weight, residual_out, y) || (uintptr_t)q % 8 || (uintptr_t)rstd % 4 ||
+      !scale_at(scale, scale_type))
+    return MOE_EINVAL;
   if (N == 0) return MOE_OK;
   hipStream_t st = (hipStream_t)stream;
   Bracket b(MOE_KERNEL_RMSNORM, st);
@@ -109,6 +120,8 @@ moe_status moe_rmsnorm_backward(const void *dy, const void *r, const void *weigh
   if (N < 0) return MOE_EINVAL;
   if (!dtype_ok(dt) || !row_ok(H)) return MOE_EUNSUPPORTED;
   if (!dweight || (N > 0 && (!dy || !r || !weight || !rstd || !dx))) return MOE_EINVAL;
+  if (!at16(dy, r, weight, dresidual, dx, dweight, workspace) || (uintptr_t)rstd % 4)
+    return MOE_EINVAL;
   const size_t need = moe_rmsnorm_backward_workspace(N, H);
   if (workspace_bytes < need || (need > 0 && !workspace)) return MOE_ENOSPC;
   hipStream_t st = (hipStream_t)stream;
@@ -131,6 +144,8 @@ moe_status moe_grouped_gemm_fp8(const moe_metadata *meta, const void *a, const v
   if (!side_ok(K, 1 << 20) || !side_ok(C, 1 << 21)) return MOE_EUNSUPPORTED;
   const bool any = meta->N > 0 && meta->capacity > 0;
   if (any && (!a || !a_scale || !w || !w_scale || !out)) return MOE_EINVAL;
+  if (!at16(a, w, out) || !scale_at(a_scale, a_scale_type) || !scale_at(w_scale, w_scale_type))
+    return MOE_EINVAL;
   if (!any) return MOE_OK;
   Fp8Args g = fp8_args(meta, K, C);
   g.a = (const uint8_t *)a;
@@ -166,6 +181,9 @@ moe_status moe_expert_forward_fp8(const moe_metadata *meta, const void *x, const
   if (!side_ok(H, 1 << 20) || !side_ok(I, 1 << 20)) return MOE_EUNSUPPORTED;
   if (meta->N > 0 &&
       (!x || !x_scale || !w_up || !w_up_scale || !w_down || !w_down_scale || !out))
+    return MOE_EINVAL;
+  if (!at16(x, w_up, w_down, h_save, out, workspace) || !scale_at(x_scale, x_scale_type) ||
+      !scale_at(w_up_scale, w_scale_type) || !scale_at(w_down_scale, w_scale_type))
     return MOE_EINVAL;
   const Fp8Ws L = fp8_layout(meta, H, I);
   if (workspace_bytes < L.total || (L.total > 0 && !workspace)) return MOE_ENOSPC;

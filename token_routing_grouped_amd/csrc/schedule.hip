@@ -84,26 +84,37 @@ int gemm_grid_f32(GemmKind kind, const GemmArgs &g) {
   return grid > 0x7fffffff ? -1 : (int)grid;
 }
 
-// 8-bit products. Few rows per expert on average (from the capacity): 16 or 32 x 128 tiles of
-// the weight-streaming kernel, else 256 x 256. Measured, the expert layer at H 7168, I 2048, 32
-// experts: 8 rows 278 us with 16-row tiles against 371 with 256; 16 rows 318 with 32-row tiles
-// against 366; 24 rows 406 against 395. At H 2048, I 512: 16 rows 58 against 64, 24 rows 69
-// against 63.
-bool fp8_skinny(const Fp8Args &g) { return (int64_t)g.cap <= 20 * (int64_t)g.E; }
+// Row tiles of every segment, bounded from the capacity, times column tiles.
+static int64_t fp8_tiles(const Fp8Args &g, int bt, int bn) {
+  int64_t mt = ((int64_t)g.cap + (int64_t)g.E * (bt - 1)) / bt;
+  if (mt > g.cap) mt = g.cap;  // no segment of a tile is empty
+  return mt * (((int64_t)g.C + bn - 1) / bn);
+}
+
+// 8-bit products. The weight-streaming kernel's tiles of 16 or 32 x 128 where there are few
+// rows per expert on average (from the capacity), and where those tiles number no more than
+// the CUs: there 256 x 256 tiles would leave most of the chip idle. Else 256 x 256. Measured:
+// the expert layer at H 7168, I 2048, 32 experts: 8 rows per expert 278 us with 16-row tiles
+// against 371 with 256; 16 rows 318 with 32-row tiles against 366; 24 rows 406 against 395.
+// At H 2048, I 512: 16 rows 58 against 64, 24 rows 69 against 63. One product by few tiles:
+// 12 experts, 270 rows, K 1040, 592 columns 12 us against 26; 4 experts, 200 rows, K and
+// columns 2048 23 against 26, but 600 rows (352 tiles by 32, K 2048, 2048 columns) 48
+// against 38.
+constexpr int kFp8Cus = 256;
+bool fp8_skinny(const Fp8Args &g) {
+  return (int64_t)g.cap <= 20 * (int64_t)g.E || fp8_tiles(g, 32, 128) <= kFp8Cus;
+}
 void fp8_tile(const Fp8Args &g, int *bt, int *bn) {
   const bool skinny = fp8_skinny(g);
   *bt = !skinny ? 256 : (int64_t)g.cap <= 8 * (int64_t)g.E ? 16 : 32;
   *bn = skinny ? 128 : 256;
 }
 
-// Row tiles of every segment, bounded from the capacity, times column tiles, in whole rounds
-// of the XCDs; fewer than 2^32 lanes in a launch.
+// In whole rounds of the XCDs; fewer than 2^32 lanes in a launch.
 int64_t fp8_grid(const Fp8Args &g) {
   int bt, bn;
   fp8_tile(g, &bt, &bn);
-  int64_t mt = ((int64_t)g.cap + (int64_t)g.E * (bt - 1)) / bt;
-  if (mt > g.cap) mt = g.cap;  // no segment of a tile is empty
-  const int64_t grid = (mt * (((int64_t)g.C + bn - 1) / bn) + 7) / 8 * 8;
+  const int64_t grid = (fp8_tiles(g, bt, bn) + 7) / 8 * 8;
   return grid >= (1 << 23) ? -1 : grid;
 }
 
