@@ -108,6 +108,10 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   static_assert(BT % (8 * NW) == 0 && BN % (8 * NW) == 0, "a load is of one operand");
   static_assert(!SWI || BN == 256, "a SwiGLU tile holds one block of 128 pairs");
   constexpr int F = BN / 16;  // column pieces of the tile
+  // The rows of a tile in pieces of 16, to the waves in turn. The first two and the last two
+  // pieces that a wave multiplies in a step are always there (they carry the step's loads and
+  // the next one's reads); those between are left out where the tile has no rows for them.
+  auto order = [](int t) constexpr { return t < 2 ? t : t < TT - 2 ? t + 2 : t - (TT - 4); };
   constexpr int SA = kKC * BT / NT, SW = (kKC * F * 2 + NT - 1) / NT;  // scales per thread
   static_assert(kKC * BT % NT == 0 && NT % BT == 0, "whole rounds");
   __shared__ __attribute__((aligned(128))) uint8_t smem[2 * STAGE];
@@ -122,6 +126,8 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   const int wt = wave / WN, wn = wave % WN;
   const int P = g.foff[g.E];
   if (P > g.cap) return;
+  const int ntn = (g.C + BN - 1) / BN;
+  const int stride = gridDim.x / kNumXcd;
   for (int i = tid; i <= g.E; i += NT) {
     const int o = g.foff[i];
     s_off[i] = o;
@@ -132,13 +138,11 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   __syncthreads();
   // Persistent workgroups: XCD x (= blockIdx % 8) owns one contiguous run of the tiles, which
   // its workgroups take in turn
-  const int ntn = (g.C + BN - 1) / BN;
   const int64_t G = (int64_t)s_pref[g.E] * ntn;
   const int x = blockIdx.x % kNumXcd;
   const int64_t gq = G / kNumXcd;
   const int gr = (int)(G % kNumXcd);
   const int64_t tend = (x + 1) * gq + min(x + 1, gr);
-  const int stride = gridDim.x / kNumXcd;
   int64_t L = x * gq + min(x, gr) + blockIdx.x / kNumXcd;
   if (L >= tend) return;
   // two blocks at least: a tile is entered by its first two (FAR: what is past K is zeros)
@@ -160,12 +164,14 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
     constexpr int GM = 4;
     const int gi = l / (GM * ntn), rem = l - gi * GM * ntn, gm = min(GM, mte - gi * GM);
     const int nt = rem / gm, mt = gi * GM + rem - nt * gm;
-    const int row0 = s_off[lo] + mt * BT;
+    // an expert's rows in even shares, of whole pieces
+    const int each = ((s_off[lo + 1] - s_off[lo] + mte - 1) / mte + 15) & ~15;
+    const int row0 = s_off[lo] + mt * each;
     Tile t;
     t.e = __builtin_amdgcn_readfirstlane(lo);
     t.nt = __builtin_amdgcn_readfirstlane(nt);
     t.row0 = __builtin_amdgcn_readfirstlane(row0);
-    t.rows = __builtin_amdgcn_readfirstlane(min(BT, s_off[lo + 1] - row0));
+    t.rows = __builtin_amdgcn_readfirstlane(min(each, s_off[lo + 1] - row0));
     return t;
   };
   // An opaque copy: what is derived from it is computed where it is used and not kept in
@@ -266,9 +272,9 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   // read next, and of its scales; pieces are constant offsets away.
   const int fr = lane & 15, fg = lane >> 4;
   const uint32_t fo0 = lds0 + fr * kQB + ((fg ^ (fr >> 1)) << 4);
-  uint32_t ta0 = fo0 + wt * (BT / WT) * kQB, wa0 = fo0 + (BT + wn * (BN / WN)) * kQB;
+  uint32_t ta0 = fo0 + wt * 16 * kQB, wa0 = fo0 + (BT + wn * (BN / WN)) * kQB;
   uint32_t ta1 = ta0 ^ 64, wa1 = wa0 ^ 64;
-  const uint32_t la = lds_address(s_sa) + (wt * (BT / WT) + fr) * 4;
+  const uint32_t la = lds_address(s_sa) + (wt * 16 + fr) * 4;
   const uint32_t lw = lds_address(s_sw) + wn * (TN * 8) + (HW ? (fr & 1) * 4 : 0);
   auto pair = [&](uint32_t a0, uint32_t a1, int off) {
     typedef const __attribute__((address_space(3))) i32x4 *P;
@@ -300,8 +306,8 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
     }
   };
   auto tokens_piece = [&](int si, int t) {
-    bt[t % 3] = pair(ta0, ta1, t * 16 * kQB);
-    sa[t % 3] = word(la + si * (BT * 4) + t * 64);
+    bt[t % 3] = pair(ta0, ta1, order(t) * WT * 16 * kQB);
+    sa[t % 3] = word(la + si * (BT * 4) + order(t) * WT * 64);
   };
   auto tokens_next = [&](int si) {  // the next block's first piece
     bt[TT % 3] = pair(ta0, ta1, 0);
@@ -342,7 +348,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   // Tokens past the segment repeat its first row, operands and scales, so they may store its
   // results again; where the columns fill whole tiles every store can then be issued.
   const bool even = g.C % BN == 0;
-  constexpr int STORES = SWI ? TT : TT * TN / 2;
+  constexpr int STORES = 4 * (SWI ? 1 : TN / 2);  // of the four pieces that are always there
   bool stored = false;
   for (;;) {
   const bool more = L + stride < tend;
@@ -385,6 +391,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
       x1 = SWI || FAR ? __uint_as_float(sa[t % 3]) * __uint_as_float(sn[m][1]) : x0;
     }
   };
+  const int live = (tile.rows + WT * 16 - 1) / (WT * 16);  // pieces with rows
   for (int kb = 0; kb < nk; kb++) {
     const int k = kb % kKC, len = min(kKC, nk - (kb - k));
     const bool last = k == len - 1;  // of the blocks whose scales are in this set
@@ -398,13 +405,18 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
       if (t + 1 < TT - 2) tokens_piece(si, t + 1);
       if (t + 1 == TT - 3) tokens_piece(si, TT - 2);
       if (t == TT - 3) tokens_piece(si, TT - 1);
+      if (t < 2 || order(t) < live) {
 #pragma unroll
-      for (int n = 0; n < TN; n++) {
-        multiply(n, t, n ? n - 1 : t ? TN - 1 : -1, n ? t : t - 1);
-        if (t < 2 && n % 2 == 1 && kb > 0) load(other_of(stage), EARLY + t * 2 + n / 2);
+        for (int n = 0; n < TN; n++) {
+          multiply(n, t, n ? n - 1 : t ? TN - 1 : -1, n ? t : t - 1);
+          if (t < 2 && n % 2 == 1 && kb > 0) load(other_of(stage), EARLY + t * 2 + n / 2);
+        }
+      } else if (order(t) == live || t == 2) {
+        add(TN - 1, t - 1);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    if (order(TT - 3) < live) add(TN - 1, TT - 3);
     // after an epilogue whose stores are all issued: not for those, only for the loads ahead
     // of them
     if (stored && kb == 0) wait_loads_before<STORES>();
@@ -423,7 +435,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int n = 0; n < TN; n++) {
-      multiply(n, TT - 2, n ? n - 1 : TN - 1, n ? TT - 1 : TT - 3);
+      multiply(n, TT - 2, n ? n - 1 : -1, TT - 1);
       multiply(n, TT - 1, n, TT - 2);
       weights_piece(sj, n);
       if (n == 0) tokens_next(sj);
@@ -452,7 +464,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   // 2^14 .. 2^15. fp16 keeps three bits more, so that the sum's one rounding to bf16 counts.
   static_assert(SWI || BN / WN == kYCols, "one scale per wave and row");
   auto store_rows = [&](int t) {
-    const int tok = wt * (BT / WT) + t * 16 + fr;
+    const int tok = (order(t) * WT + wt) * 16 + fr;
     const int64_t s = row0 + (tok < rows ? tok : 0);
     uint16_t *o = g.out + s * g.C;
     float by = 1.0f;
@@ -489,15 +501,16 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   };
   if constexpr (!SWI) {
 #pragma unroll
-    for (int t = 0; t < TT; t++) store_rows(t);
+    for (int t = 0; t < TT; t++)
+      if (order(t) < live) store_rows(t);
   } else {
     // a = silu(gate) up; the block of 128 is the whole tile, so a token's maximum is taken
     // over the four lanes that share it and over the WN waves
     float av[TN][TT][2];
 #pragma unroll
     for (int t = 0; t < TT; t++) {
-      const int tok = wt * (BT / WT) + t * 16 + fr;
-      if (g.out) store_rows(t);
+      const int tok = (order(t) * WT + wt) * 16 + fr;
+      if (g.out && order(t) < live) store_rows(t);
       uint32_t m = 0;
 #pragma unroll
       for (int n = 0; n < TN; n++) {
@@ -531,7 +544,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
     static_assert(TN == 4, "four pieces, one for each lane that shares a token");
 #pragma unroll
     for (int t = 0; t < TT; t++) {
-      const int tok = wt * (BT / WT) + t * 16 + fr;
+      const int tok = (order(t) * WT + wt) * 16 + fr;
       uint32_t m = s_max[0][tok];
 #pragma unroll
       for (int w = 1; w < WN; w++) m = m > s_max[w][tok] ? m : s_max[w][tok];
@@ -550,7 +563,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
       const auto q1 = __builtin_amdgcn_permlane16_swap(h0[1], h1[1], false, false);
       const u32x2 q = {q0[0] | (q0[1] << 16), q1[0] | (q1[1] << 16)};
       const int j = nt * kQB + wn * (BN / WN / 2) + fg * 8;
-      if (even || (tok < rows && j < I))
+      if (even ? order(t) < live : tok < rows && j < I)
         *(u32x2 *)(g.aq + (int64_t)(row0 + (tok < rows ? tok : 0)) * I + j) = q;
       if (wn == 0 && fg == 0 && tok < rows)
         g.aq_scale[(int64_t)(row0 + tok) * ((I + kQB - 1) / kQB) + nt] = (uint8_t)ex;
