@@ -124,8 +124,6 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wt = wave / WN, wn = wave % WN;
-  const int P = g.foff[g.E];
-  if (P > g.cap) return;
   const int ntn = (g.C + BN - 1) / BN;
   const int stride = gridDim.x / kNumXcd;
   for (int i = tid; i <= g.E; i += NT) {
@@ -134,6 +132,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
     if (i < g.E) s_pref[i] = (g.foff[i + 1] - o + BT - 1) / BT;
   }
   __syncthreads();
+  if (s_off[g.E] > g.cap) return;
   wave0_exclusive_scan(s_pref, g.E);
   __syncthreads();
   // Persistent workgroups: XCD x (= blockIdx % 8) owns one contiguous run of the tiles, which

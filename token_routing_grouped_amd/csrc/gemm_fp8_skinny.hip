@@ -46,14 +46,13 @@ __global__ __launch_bounds__(64 * NW, OCC) void skinny_kernel(Fp8Args g) {
   int *s_pref = s_tab, *s_off = s_tab + MOE_MAX_EXPERTS + 1;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int P = g.foff[g.E];
-  if (P > g.cap) return;
   for (int i = tid; i <= g.E; i += NT) {
     const int o = g.foff[i];
     s_off[i] = o;
     if (i < g.E) s_pref[i] = (g.foff[i + 1] - o + BT - 1) / BT;
   }
   __syncthreads();
+  if (s_off[g.E] > g.cap) return;
   wave0_exclusive_scan(s_pref, g.E);
   __syncthreads();
   // XCD x (= blockIdx % 8) takes one contiguous run of the tiles; an expert's row tiles of one
