@@ -99,33 +99,28 @@ hipError_t launch_gemm_fp8(bool swiglu, const Fp8Args &g, hipStream_t) {
   if (g.nbk != (int)nb(g.K) || g.nbc != (int)nb(g.C)) return hipErrorInvalidValue;
   if (g.out) wr(g.out, cap * g.C * 2);
   if (!swiglu) {
+    if (!g.out != (g.f32 != nullptr) || (g.f32 && !fp8_skinny(g))) return hipErrorInvalidValue;
+    if (g.f32) wr(g.f32, cap * g.C * 4);
     if (g.ys) wr(g.ys, cap * ((g.C + kYCols - 1) / kYCols));
   } else if (fp8_skinny(g)) {
-    wr(g.af, cap * (g.C / 2) * 4);
+    wr(g.f32, cap * (g.C / 2) * 4);
   } else {
     wr(g.aq, cap * (g.C / 2));
     wr(g.aq_scale, cap * nb(g.C / 2));
   }
   return hipSuccess;
 }
-static hipError_t combine(const void *y, const uint8_t *ys, const int32_t *tok_off, const int32_t *s_rev,
-                          const float *scores, int N, int H, int cap, void *out) {
+hipError_t launch_combine_to_bf16(const void *y, const uint8_t *ys, const int32_t *tok_off,
+                                  const int32_t *s_rev, const float *scores, int N, int H, int cap, void *out,
+                                  hipStream_t) {
   g_launches++;
-  rd(y, (size_t)cap * H * 2);
+  rd(y, (size_t)cap * H * (ys ? 2 : 4));
   if (ys) rd(ys, (size_t)cap * ((H + kYCols - 1) / kYCols));
   rd(tok_off, (size_t)(N + 1) * 4);
   rd(s_rev, (size_t)cap * 4);
   rd(scores, (size_t)cap * 4);
   wr(out, (size_t)N * H * 2 + (g_plant ? 2 : 0));
   return hipSuccess;
-}
-hipError_t launch_combine_f16(const void *y, const uint8_t *ys, const int32_t *tok_off, const int32_t *s_rev,
-                              const float *scores, int N, int H, int cap, void *out, hipStream_t) {
-  return combine(y, ys, tok_off, s_rev, scores, N, H, cap, out);
-}
-hipError_t launch_combine(bool, const void *y, const int32_t *tok_off, const int32_t *s_rev,
-                          const float *scores, int N, int H, int cap, void *out, hipStream_t) {
-  return combine(y, nullptr, tok_off, s_rev, scores, N, H, cap, out);
 }
 
 }  // namespace moe

@@ -99,8 +99,8 @@ def test_grouped_product_refusals():
 def test_expert_forward_refusals():
     f, ws = L().moe_expert_forward_fp8, L().moe_expert_forward_fp8_workspace
     need = ws(meta(), 64, 32)
-    assert need == 256 + 256 + 8 * 64 * 2 + 8 * 32 * 4
-    assert ws(meta(cap=61), 64, 32) == 2048 + 256 + 7936 + 7936  # few tiles of 32 rows
+    assert need == 256 + 256 + 8 * 64 * 4 + 8 * 32 * 4
+    assert ws(meta(cap=61), 64, 32) == 2048 + 256 + 15616 + 7936  # few tiles of 32 rows
     n = 1 << 16  # neither few rows per expert nor few tiles
     assert ws(meta(cap=n), 64, 32) == n * 32 + n + n * 64 * 2 + n
 

@@ -37,7 +37,7 @@ Fp8Args fp8_args(const moe_metadata *m, int32_t K, int32_t C) {
 }
 
 struct Fp8Ws {
-  size_t aq, as, y, ys, af, total;
+  size_t aq, as, y, ys, a32, total;
 };
 Fp8Ws fp8_layout(const moe_metadata *m, int32_t H, int32_t I) {
   const size_t cap = (size_t)m->capacity;
@@ -45,11 +45,11 @@ Fp8Ws fp8_layout(const moe_metadata *m, int32_t H, int32_t I) {
   w.aq = 0;
   w.as = w.aq + align_up(cap * (size_t)I);
   w.y = w.as + align_up(cap * (size_t)blocks(I));
-  // kernel for few rows: up, a in fp32 first; down, no scales of y
+  // the kernel for few rows: a in fp32 first; y in fp32, else in fp16 with scales
   const bool up = fp8_skinny(fp8_args(m, H, 2 * I)), down = fp8_skinny(fp8_args(m, I, H));
-  w.ys = w.y + align_up(cap * (size_t)H * 2);
-  w.af = w.ys + (down ? 0 : align_up(cap * (size_t)((H + kYCols - 1) / kYCols)));
-  w.total = w.af + (up ? align_up(cap * (size_t)I * sizeof(float)) : 0);
+  w.ys = w.y + align_up(cap * (size_t)H * (down ? sizeof(float) : 2));
+  w.a32 = w.ys + (down ? 0 : align_up(cap * (size_t)((H + kYCols - 1) / kYCols)));
+  w.total = w.a32 + (up ? align_up(cap * (size_t)I * sizeof(float)) : 0);
   return w;
 }
 
@@ -203,7 +203,7 @@ moe_status moe_expert_forward_fp8(const moe_metadata *meta, const void *x, const
   up.out = (uint16_t *)h_save;
   up.aq = ws + L.aq;
   up.aq_scale = ws + L.as;
-  up.af = (float *)(ws + L.af);
+  up.f32 = (float *)(ws + L.a32);
   up.concat = layout == MOE_GATEUP_CONCAT;
   Fp8Args dn = fp8_args(meta, I, H);
   dn.a = up.aq;
@@ -213,8 +213,12 @@ moe_status moe_expert_forward_fp8(const moe_metadata *meta, const void *x, const
   dn.w = (const uint8_t *)w_down;
   dn.w_scale = w_down_scale;
   dn.w_e8m0 = up.w_e8m0;
-  dn.out = (uint16_t *)(ws + L.y);
-  dn.ys = fp8_skinny(dn) ? nullptr : ws + L.ys;
+  if (fp8_skinny(dn)) {
+    dn.f32 = (float *)(ws + L.y);
+  } else {
+    dn.out = (uint16_t *)(ws + L.y);
+    dn.ys = ws + L.ys;
+  }
   if (fp8_grid(up) < 0 || fp8_grid(dn) < 0) return MOE_EUNSUPPORTED;
   if (meta->capacity > 0) {
     Bracket b(MOE_KERNEL_UP_SWIGLU_FP8, st);
@@ -222,7 +226,7 @@ moe_status moe_expert_forward_fp8(const moe_metadata *meta, const void *x, const
   }
   if (meta->capacity > 0 && fp8_skinny(up)) {  // rows past the last pair: never read
     Bracket b(MOE_KERNEL_QUANT_ROWS, st);
-    if (launch_quantize_rows(up.af, meta->capacity, I, false, up.aq, up.aq_scale, 1, st) !=
+    if (launch_quantize_rows(up.f32, meta->capacity, I, false, up.aq, up.aq_scale, 1, st) !=
         hipSuccess)
       return MOE_EHIP;
   }
@@ -233,9 +237,7 @@ moe_status moe_expert_forward_fp8(const moe_metadata *meta, const void *x, const
   Bracket b(MOE_KERNEL_COMBINE, st);
   const int32_t *off = meta->num_activated_expert_per_token_offset;
   const int32_t *rev = meta->s_reverse_scatter_idx;
-  return status_of(dn.ys ? launch_combine_f16(dn.out, dn.ys, off, rev, meta->router_scores, meta->N, H,
-                                              meta->capacity, out, st)
-                         : launch_combine(true, dn.out, off, rev, meta->router_scores, meta->N, H,
+  return status_of(launch_combine_to_bf16(ws + L.y, dn.ys, off, rev, meta->router_scores, meta->N, H,
                                           meta->capacity, out, st));
 }
 

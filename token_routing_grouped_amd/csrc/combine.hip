@@ -78,6 +78,18 @@ struct Vec<F16> {
   __device__ static u32x4 pack(const float *f) { return Vec<uint16_t>::pack(f); }
 };
 
+struct F32 {  // fp32, rounded to bf16 at the end
+  float v;
+};
+template <>
+struct Vec<F32> {
+  static constexpr int n = 4;
+  __device__ static void add(const u32x4 &v, float w, float *f) { Vec<float>::add(v, w, f); }
+  __device__ static u32x2 pack(const float *f) {
+    return u32x2{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
+  }
+};
+
 struct DscoreArgs {
   const int32_t *topk_idx;
   int K, E;
@@ -110,7 +122,8 @@ __global__ __launch_bounds__(CT) void combine_kernel(const T *__restrict__ y,
   const float my_w = lane < n ? (scores ? scores[q0 + lane] : 1.0f) : 0.0f;
 
   const int nchunk = H / V;
-  u32x4 *orow = (u32x4 *)(out + (int64_t)t * H);
+  using Out = decltype(Vec<T>::pack(nullptr));  // a chunk of the output
+  Out *orow = (Out *)out + (int64_t)t * nchunk;
   for (int c0 = blockIdx.y * 64 * CHUNKS; c0 < nchunk; c0 += gridDim.y * 64 * CHUNKS) {
     float acc[CHUNKS][V];
 #pragma unroll
@@ -205,20 +218,27 @@ hipError_t launch_combine(bool bf16, const void *y, const int32_t *tok_off, cons
   return launch<false>(bf16, y, tok_off, s_rev, scores, N, H, cap, out, ds, stream);
 }
 
-hipError_t launch_combine_f16(const void *y, const uint8_t *ys, const int32_t *tok_off,
-                              const int32_t *s_rev, const float *scores, int N, int H, int cap,
-                              void *out, hipStream_t stream) {
-  if (N == 0) return hipSuccess;
+template <typename T>
+hipError_t launch_to_bf16(const void *y, const uint8_t *ys, const int32_t *tok_off,
+                          const int32_t *s_rev, const float *scores, int N, int H, int cap,
+                          void *out, hipStream_t stream) {
   const int grid = (N + 3) / 4;
   if (N < kSplitTokens)
-    hipLaunchKernelGGL((combine_kernel<F16, false, 1, 8>), dim3(grid, (H / 8 + 63) / 64), dim3(CT), 0,
-                       stream, (const F16 *)y, tok_off, s_rev, scores, N, H, cap, (F16 *)out,
-                       DscoreArgs{}, ys);
+    hipLaunchKernelGGL((combine_kernel<T, false, 1, 8>),
+                       dim3(grid, (H / Vec<T>::n + 63) / 64), dim3(CT), 0, stream, (const T *)y,
+                       tok_off, s_rev, scores, N, H, cap, (T *)out, DscoreArgs{}, ys);
   else
-    hipLaunchKernelGGL((combine_kernel<F16, false, 4, 2>), dim3(grid), dim3(CT), 0, stream,
-                       (const F16 *)y, tok_off, s_rev, scores, N, H, cap, (F16 *)out, DscoreArgs{},
-                       ys);
+    hipLaunchKernelGGL((combine_kernel<T, false, 4, 2>), dim3(grid), dim3(CT), 0, stream,
+                       (const T *)y, tok_off, s_rev, scores, N, H, cap, (T *)out, DscoreArgs{}, ys);
   return hipGetLastError();
+}
+
+hipError_t launch_combine_to_bf16(const void *y, const uint8_t *ys, const int32_t *tok_off,
+                                  const int32_t *s_rev, const float *scores, int N, int H, int cap,
+                                  void *out, hipStream_t stream) {
+  if (N == 0) return hipSuccess;
+  return ys ? launch_to_bf16<F16>(y, ys, tok_off, s_rev, scores, N, H, cap, out, stream)
+            : launch_to_bf16<F32>(y, ys, tok_off, s_rev, scores, N, H, cap, out, stream);
 }
 
 hipError_t launch_combine_dscore(bool bf16, const void *dxg, const int32_t *tok_off,

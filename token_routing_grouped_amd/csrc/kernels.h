@@ -151,11 +151,11 @@ hipError_t launch_gemm_f32(GemmKind kind, const GemmArgs &g, hipStream_t stream)
 hipError_t launch_combine(bool bf16, const void *y, const int32_t *tok_off,
                           const int32_t *s_rev, const float *scores, int N, int H, int cap,
                           void *out, hipStream_t stream);
-// The same from fp16 y with a scale per row and kYCols columns (its exponent e: y stands for
-// y 2^(e - 141)), to bf16.
-hipError_t launch_combine_f16(const void *y, const uint8_t *ys, const int32_t *tok_off,
-                              const int32_t *s_rev, const float *scores, int N, int H, int cap,
-                              void *out, hipStream_t stream);
+// The same to bf16 from fp32 y (ys null), or from fp16 y with a scale per row and kYCols
+// columns (its exponent e: y stands for y 2^(e - 141)).
+hipError_t launch_combine_to_bf16(const void *y, const uint8_t *ys, const int32_t *tok_off,
+                                  const int32_t *s_rev, const float *scores, int N, int H, int cap,
+                                  void *out, hipStream_t stream);
 // The same for dx with unit weights, also writing d_topk_weights[t,k] = the sum over
 // column tiles of partial[s_rev[q],tile] for the slot's pair q (0 at invalid slots).
 hipError_t launch_combine_dscore(bool bf16, const void *dxg, const int32_t *tok_off,
@@ -199,12 +199,14 @@ struct Fp8Args {
   const void *w_scale;
   int a_e8m0, w_e8m0;
   int nbk, nbc;  // blocks along K and C
-  uint16_t *out;  // bf16 [cap,C]; SwiGLU: h_save, or null
+  uint16_t *out;  // bf16 [cap,C]; SwiGLU: h_save, or null; null where f32 takes the results
   uint8_t *ys;    // down projection, 256-wide tiles: out is fp16 with scales [cap, ceil(C/kYCols)]
   // SwiGLU: C = 2I; a = silu(gate) up in e4m3 [cap,I] with e8m0 scales [cap, ceil(I/128)]
   uint8_t *aq;
   uint8_t *aq_scale;
-  float *af;   // few rows per expert: a in fp32 [cap,I] instead, put in 8 bits by its own pass
+  // few rows or tiles: results in fp32 instead, a [cap,I], put in 8 bits by its own pass, or y
+  // [cap,C] for the combine (few rows' y costs no time; its sum is rounded once)
+  float *f32;
   int concat;  // rows of w (and its scale blocks) are [gates | ups]
 };
 // whether the products take the kernel for few rows per expert, rows and columns of a tile, and the workgroups of a launch (-1: too many)

@@ -4,12 +4,16 @@
 // as bf16 or fp32, in e4m3 with a power-of-two scale per 128 values, or both. Bound by
 // memory. A row is held in the registers of TPR lanes between its one read and its
 // writes: eight values per lane and chunk, so the 16 lanes of a DPP row hold one block of
-// 128 and its maximum needs no LDS. Rows too long for that are read a second time.
+// 128 and its maximum needs no LDS. Rows too long for that are read a second time. Measured:
+// 16384 x 2048 bf16 with a residual, to r, y and 8 bits (303 MB): 61 us, 5.0 TB/s, as a large
+// copy; one row of 7168: 5.2 us, the launch and one trip to memory and back.
 //
 // Backward: with g = dy weight and c = mean(g r) rstd^2, dx = rstd (g - r c) + dresidual;
 // dweight = sum over rows of dy r rstd. Bound by memory. A workgroup walks rows a grid
 // apart with the columns fixed to its threads, so its share of dweight stays in registers;
 // the shares are written once and a second launch adds them in a fixed order (no atomics).
+// Measured: 16384 x 2048 bf16 with the residual's gradient (269 MB) 55 us, 4.9 TB/s, and 5 us
+// for the shares; 333 x 5000 fp32 9 us and 4 us.
 #include "fp8.h"
 #include "kernels.h"
 
