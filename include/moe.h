@@ -207,7 +207,9 @@ moe_status moe_expert_backward(const moe_metadata *meta, const int32_t *topk_idx
  *
  * Addresses. Tensors and workspaces of these calls start at multiples of 16 bytes (what
  * moe_quantize_rows and the norm write as q: of 8), fp32 scales and rstd of 4, e8m0 scales
- * anywhere; MOE_EINVAL otherwise. Apart from the outputs that are said to be allowed in the
+ * anywhere; MOE_EINVAL otherwise. Sizes. MOE_EUNSUPPORTED where one launch does not hold
+ * the work: N ceil(H/128) from 2^28 on in moe_quantize_rows, E ceil(K/128) ceil(C/128) from
+ * 2^24 on in moe_quantize_weights, 2^23 tiles in the products. Apart from the outputs that are said to be allowed in the
  * place of an input, outputs and inputs do not overlap. */
 typedef enum { MOE_SCALE_FP32 = 0, MOE_SCALE_E8M0 = 1 } moe_scale_type;
 enum { MOE_QBLOCK = 128 };
