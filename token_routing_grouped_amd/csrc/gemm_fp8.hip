@@ -20,9 +20,8 @@
 // SIMD's two waves. One workgroup per CU stays for the whole launch and takes its tiles in
 // turn, so that a tile's first blocks are loaded under the epilogue of the one before. An
 // expert's rows are shared out evenly over its tiles, and 16-row pieces without rows are not
-// multiplied (uneven experts: 538 us against 575 with tiles of 256 rows and a rest; smaller
-// shares, down to 128 rows, were measured slower even where they filled the CUs more evenly,
-// since a step's weights stay the same: 91 us against 63 for 24k rows, K 2048, 1024 columns).
+// multiplied (uneven experts: 538 us against 575 with tiles of 256 rows and a rest). Where a
+// few rounds of tiles leave many CUs idle in the last one, the shares are smaller (kStepRows).
 //
 // LDS holds two stages of 256 + 256 rows of 128 bytes, filled by direct global-to-LDS loads one
 // block ahead of the products, in eighths between them. The 16-byte chunk c of row r lies at
@@ -76,6 +75,18 @@ __device__ __forceinline__ uint32_t lds_address(const void *p) {
       (int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p);
 }
 
+// The choice of a tile's rows, 256 down to 128: fewer where the rounds of tiles that the
+// workgroups make are then better filled. A step costs as much for its weights as for
+// kStepRows of its rows (measured: with 128 rows 74 % of its time with 256); rows are counted as
+// the mean of the most and of the average, and what is not 6 % better is not worth it. 24k
+// rows (763 an expert), K 2048, 1024 columns: 63 us with 256, 57.5 with 224 (chosen), 75 with
+// 192; K 512, 2048 columns: 48.6, 45.1 (chosen), 51. 33k rows (1024 an expert), K 2048: 85.6,
+// 80.8, 78.8 (chosen); K 512: 59.8 (chosen), 63.9, 60.9. 9k rows: 35.1, 32.1, 31.9 (chosen).
+constexpr float kStepRows = 236.0f, kWorth = 0.94f;
+// row tiles of n rows, at most `most` each (n < 2^31, most of 128 to 256)
+__device__ __forceinline__ int tiles_of(int n, int most) {
+  return (int)(((uint32_t)n + (uint32_t)most - 1) / (uint32_t)most);
+}
 constexpr int kKC = 8;  // blocks of K whose scales LDS holds at a time (two such sets)
 
 // Four lanes that share a token (16 apart) hold four consecutive bf16 columns each of pieces
@@ -128,12 +139,14 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   // pieces that a wave multiplies in a step are always there (they carry the step's loads and
   // the next one's reads); those between are left out where the tile has no rows for them.
   auto order = [](int t) constexpr { return t < 2 ? t : t < TT - 2 ? t + 2 : t - (TT - 4); };
+  constexpr int SIZES = 5;  // of a tile's rows
   constexpr int SA = kKC * BT / NT, SW = (kKC * F * 2 + NT - 1) / NT;  // scales per thread
   static_assert(kKC * BT % NT == 0 && NT % BT == 0, "whole rounds");
   __shared__ __attribute__((aligned(128))) uint8_t smem[2 * STAGE];
   __shared__ uint32_t s_sa[2][kKC][BT];    // token scales (bits: e8m0 byte or fp32)
   __shared__ uint32_t s_sw[2][kKC][F][2];  // weight scales of a piece's even and odd rows
   __shared__ uint32_t s_max[SWI ? WN : 1][SWI ? BT : 1];  // a token's largest |a|, per wave
+  __shared__ int s_num[SIZES];
   __shared__ int s_tab[2 * (MOE_MAX_EXPERTS + 1)];
   int *s_pref = s_tab, *s_off = s_tab + MOE_MAX_EXPERTS + 1;
 
@@ -145,10 +158,37 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   for (int i = tid; i <= g.E; i += NT) {
     const int o = g.foff[i];
     s_off[i] = o;
-    if (i < g.E) s_pref[i] = (g.foff[i + 1] - o + BT - 1) / BT;
   }
   __syncthreads();
   if (s_off[g.E] > g.cap) return;
+  // Rows of a tile at most: wave j counts the tiles of at most BT - 32 j rows.
+  static_assert(SIZES <= NW, "a wave for each");
+  if (wave < SIZES) {
+    const int most = BT - 32 * wave;
+    int n = 0;
+    for (int i = lane; i < g.E; i += 64) n += tiles_of(s_off[i + 1] - s_off[i], most);
+    n = wave_inclusive_scan_dpp(n);
+    if (lane == 63) s_num[wave] = n;
+  }
+  __syncthreads();
+  int most = BT;
+  {
+    const float per = (float)ntn / (float)(kNumXcd * stride), total = (float)s_off[g.E];
+    float best = 0.0f;
+#pragma unroll
+    for (int j = 0; j < SIZES; j++) {
+      const int rows = BT - 32 * j;
+      const float n = (float)s_num[j];  // (no tiles: any choice)
+      const float cost = ceilf(n * per - 1e-3f) * (kStepRows + 0.5f * ((float)rows + total / n));
+      if (j == 0 || cost < best) {
+        best = j == 0 ? cost * kWorth : cost;
+        most = rows;
+      }
+    }
+  }
+  most = __builtin_amdgcn_readfirstlane(most);
+  for (int i = tid; i < g.E; i += NT) s_pref[i] = tiles_of(s_off[i + 1] - s_off[i], most);
+  __syncthreads();
   wave0_exclusive_scan(s_pref, g.E);
   __syncthreads();
   // Persistent workgroups: XCD x (= blockIdx % 8) owns one contiguous run of the tiles, which

@@ -209,7 +209,8 @@ struct Fp8Args {
   float *f32;
   int concat;  // rows of w (and its scale blocks) are [gates | ups]
 };
-// whether the products take the kernel for few rows per expert, rows and columns of a tile, and the workgroups of a launch (-1: too many)
+// Whether the products take the kernel for few rows per expert or few tiles, the fewest rows and
+// the columns of a tile, and the workgroups that such tiles would take (-1: too many).
 bool fp8_skinny(const Fp8Args &g);
 void fp8_tile(const Fp8Args &g, int *bt, int *bn);
 int64_t fp8_grid(const Fp8Args &g);

@@ -106,7 +106,7 @@ bool fp8_skinny(const Fp8Args &g) {
 }
 void fp8_tile(const Fp8Args &g, int *bt, int *bn) {
   const bool skinny = fp8_skinny(g);
-  *bt = !skinny ? 256 : (int64_t)g.cap <= 8 * (int64_t)g.E ? 16 : 32;
+  *bt = !skinny ? 128 : (int64_t)g.cap <= 8 * (int64_t)g.E ? 16 : 32;
   *bn = skinny ? 128 : 256;
 }
 
