@@ -233,7 +233,8 @@ moe_status moe_quantize_weights(const void *w, int32_t E, int32_t K, int32_t C, 
  * with a residual, NULL without; it may be x or residual itself). y [N,H] (dt), or NULL;
  * q [N,H] e4m3 with scale [N, ceil(H/128)], or NULL; one of the two at least. Both are
  * rounded from the unrounded fp32 y. rstd [N] fp32, or NULL (the backward takes it).
- * H a positive multiple of 8 up to 2^20; eps >= 0. Sums are fp32 in a fixed order. */
+ * H a positive multiple of 8 up to 2^20; eps >= 0. Squares and sums are fp32, in a fixed
+ * order (|r| from 2^63 on overflows them: y is 0 there). */
 moe_status moe_rmsnorm_forward(const void *x, const void *residual, const void *weight,
                                float eps, int32_t N, int32_t H, moe_dtype dt,
                                void *residual_out, void *y, void *q, void *scale,

@@ -281,7 +281,16 @@ __global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float *__restric
   const int c = blockIdx.x * 64 + l * 4;
   f32x4 v = {0, 0, 0, 0};
   if (c < H)
-    for (int g = grp; g < G; g += 64) v += *(const f32x4 *)(part + (int64_t)g * H + c);
+    for (int g0 = grp; g0 < G; g0 += 512) {  // eight shares' loads at a time
+      f32x4 p[8];
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        const int g = g0 + 64 * i;
+        p[i] = g < G ? *(const f32x4 *)(part + (int64_t)g * H + c) : f32x4{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int i = 0; i < 8; i++) v += p[i];
+    }
   *(f32x4 *)&s[grp][l * 4] = v;
   __syncthreads();
   if (threadIdx.x < 64) {
