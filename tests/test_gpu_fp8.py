@@ -271,6 +271,8 @@ SHAPES = [  # N, K, C, E, topk, p_invalid
     (5200, 256, 2064, 3, 2, 0.0),
     (5200, 384, 2048, 3, 2, 0.1),
     (1300, 128, 1024, 40, 1, 0.0),
+    (2500, 256, 1024, 80, 1, 0.0),  # several tiles to a workgroup, of few rows each
+    (6000, 400, 1024, 80, 1, 0.0),
 ]
 
 
@@ -459,6 +461,8 @@ EXPERTS = [  # N, H, I, E, topk, p_invalid
     (2000, 272, 144, 3, 2, 0.1),   # from here on for both
     (2500, 384, 256, 4, 2, 0.0),
     (6400, 256, 1024, 3, 2, 0.0),  # more tiles than CUs
+    (2500, 512, 512, 80, 1, 0.0),  # and of few rows each
+    (6000, 256, 512, 80, 1, 0.0),
 ]
 
 

@@ -629,7 +629,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   }
   if (!more) break;
   L += stride;
-  stored = even;
+  stored = even && live >= 4;  // STORES of them, at least
   tile = next;
   }  // tiles
 }
