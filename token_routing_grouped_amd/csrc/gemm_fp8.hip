@@ -406,7 +406,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   // Tokens past the segment repeat its first row, operands and scales, so they may store its
   // results again; where the columns fill whole tiles every store can then be issued.
   const bool even = g.C % BN == 0;
-  constexpr int STORES = 4 * (SWI ? 1 : TN / 2);  // of the four pieces that are always there
+  constexpr int STORES = 4 * (SWI ? 1 : TN / 2);  // of four pieces of rows
   bool stored = false;
   for (;;) {
   const bool more = L + stride < tend;
@@ -629,7 +629,7 @@ __global__ __launch_bounds__(64 * WT * WN, 2) void gemm_fp8_kernel(Fp8Args g) {
   }
   if (!more) break;
   L += stride;
-  stored = even && live >= 4;  // STORES of them, at least
+  stored = even && live >= 4;  // STORES of them at least, behind the loads
   tile = next;
   }  // tiles
 }
